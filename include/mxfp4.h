@@ -168,7 +168,7 @@ typedef enum {
 #define MXFP4_COLS_ROWMAJOR 0
 #define MXFP4_COLS_MMA 1
 
-#define MXFP4_ABI_VERSION 5
+#define MXFP4_ABI_VERSION 6
 
 /*
  * Arguments of one QDQ call. Zero-initialise and fill what is used; every
@@ -414,6 +414,230 @@ typedef struct mxfp4_dual_level_args {
 } mxfp4_dual_level_args;
 
 mxfp4_status mxfp4_dual_level_qdq(const mxfp4_dual_level_args* args, mxfp4_stream_t stream);
+
+/*
+ * ---- Mixture-of-experts layer around the grouped GEMM --------------------
+ *
+ * The four operators below take tokens to their experts and back: routing
+ * chooses experts and lays out the expert-sorted order of the (token, expert)
+ * pairs, whose counts are a group_list (type 1) of this library; dispatch
+ * copies (or quantises) token rows into that order; the grouped linear
+ * multiplies and applies bias, activation and residual; combine adds the
+ * result rows back per token. All of them allocate nothing, are asynchronous
+ * on `stream`, return argument errors before any launch and write the same
+ * bytes for the same inputs every time. Zero-initialise an argument struct
+ * and fill what is used.
+ */
+
+/* Scores of mxfp4_moe_route_args.score. */
+#define MXFP4_SCORE_SOFTMAX 0
+#define MXFP4_SCORE_SIGMOID 1
+/* Ranks of expert groups (mxfp4_moe_route_args.group_score). */
+#define MXFP4_GROUP_BEST 0 /* the group's largest key */
+#define MXFP4_GROUP_TOP2 1 /* the sum of its two largest keys (its only one, if one expert is open) */
+#define MXFP4_MOE_MAX_EXPERTS 1024
+#define MXFP4_MOE_MAX_K 32
+#define MXFP4_MOE_MAX_EXPERT_GROUPS 32
+
+/*
+ * Routing. Per token with logits x_0 .. x_{E-1} (fp32 or bf16):
+ *   score   s_e = softmax(x)_e or 1 / (1 + exp(-x_e))
+ *   key     s_e + bias_e (bias NULL: s_e), evaluated in 64 bits; an expert is
+ *           closed to the token when x_e is -inf or bias_e is not finite
+ *   groups  with num_groups > 1 the experts form num_groups runs of E /
+ *           num_groups; the topk_groups groups of greatest rank
+ *           (group_score; ties: the lower group) stay open
+ *   choice  the k open experts of greatest key, in that order (ties: the lower
+ *           expert); slots without an open expert hold expert -1, weight 0
+ *   weight  scale * s_e, with renormalize scale * s_e / (sum of the chosen s)
+ * A token whose token_mask byte is 0 gets no expert (its logits are not
+ * read). A token with a NaN or +inf logit gets experts 0 .. k-1 and NaN weights.
+ * Order: row r of the expert-sorted order belongs to pair slots[r] = token * k
+ * + slot; pairs are sorted by expert, then by token; rows[token][slot] is a
+ * pair's row (-1 for expert -1), slots[r] is -1 behind the last row, and
+ * counts[e] is the number of expert e's rows.
+ *   logits      [tokens][experts], leading dimension ld; dtype MXFP4_F32 / MXFP4_BF16.
+ *   bias        optional fp32 [experts]; token_mask optional [tokens] bytes.
+ *   weights     fp32 [tokens][k]; chosen, rows int32 [tokens][k];
+ *   slots       int32 [tokens * k]; counts int64 [experts].
+ *   workspace   mxfp4_moe_route_workspace(tokens, experts) bytes, 4-byte
+ *               aligned (may be NULL when that is 0); its contents matter
+ *               to this call only.
+ * Limits: experts <= 1024, k <= 32, num_groups <= 32, tokens * k < 2^31.
+ *
+ * mxfp4_moe_route_bwd: grad_logits [tokens][experts] (leading dimension
+ * ld_grad, dtype as logits) from grad_weights fp32 [tokens][k], for the chosen
+ * experts given in `chosen` (read; the choice itself and the bias have no
+ * gradient). Rows of tokens without an expert are zero; rows with a NaN or
+ * +inf logit are NaN.
+ */
+typedef struct mxfp4_moe_route_args {
+    const void* logits;
+    int64_t tokens;
+    int64_t experts;
+    int64_t ld;
+    int32_t dtype;
+    int32_t k;
+    int32_t score;
+    int32_t renormalize;
+    float scale;
+    int32_t num_groups;
+    int32_t topk_groups;
+    int32_t group_score;
+    const float* bias;
+    const uint8_t* token_mask;
+    float* weights;
+    int32_t* chosen;
+    int32_t* rows;
+    int32_t* slots;
+    int64_t* counts;
+    void* workspace;
+    int64_t workspace_bytes;
+    const float* grad_weights;
+    void* grad_logits;
+    int64_t ld_grad;
+} mxfp4_moe_route_args;
+
+int64_t mxfp4_moe_route_workspace(int64_t tokens, int64_t experts);
+mxfp4_status mxfp4_moe_route(const mxfp4_moe_route_args* args, mxfp4_stream_t stream);
+mxfp4_status mxfp4_moe_route_bwd(const mxfp4_moe_route_args* args, mxfp4_stream_t stream);
+
+/*
+ * Dispatch and combine. rows int32 [tokens][k] is the index list of
+ * mxfp4_moe_route: the row of each (token, slot) among row_count expert rows.
+ * An index outside [0, row_count) is skipped; rows that no index names are
+ * left as they were. The indices in range must differ from one another (an
+ * index named twice receives one of the two rows).
+ *
+ * mxfp4_moe_dispatch: row rows[t][j] of the outputs = row t of x,
+ *   values      x's dtype, [row_count][cols], leading dimension ld_out, and / or
+ *   codes, scales  x quantised along its rows as mxfp4_qdq_fwd does with block
+ *               32 (elem_format, scale_mode, scale_factor): codes
+ *               [row_count][ceil(cols/2)] (E2M1) or [row_count][cols] (E4M3)
+ *               bytes, E8M0 scales in the MXFP4_SCALES_MMA layout of
+ *               [row_count][ceil(cols/32)], whose padding (block columns
+ *               behind the last one in the rows written, and rows behind
+ *               row_count) is written as 0.
+ *
+ * mxfp4_moe_combine: out[t] = residual[t] + sum_j weights[t][j] y[rows[t][j]],
+ *   summed in fp32 in the slots' order, rounded once. weights NULL: ones;
+ *   residual NULL: none. y [row_count][cols], leading dimension ld_rows.
+ *
+ * mxfp4_moe_combine_bwd: from grad_out [tokens][cols] (ld_out):
+ *   grad_rows[rows[t][j]] = weights[t][j] grad_out[t] (leading dimension
+ *   ld_grad_rows) and grad_weights[t][j] = grad_out[t] . y[rows[t][j]] (fp32;
+ *   0 for a skipped index); either may be NULL. The residual's gradient is
+ *   grad_out; the gradient of a dispatch of values is a combine without
+ *   weights.
+ * Limits: k <= 32, tokens * k < 2^31, row_count < 2^31.
+ */
+typedef struct mxfp4_moe_move_args {
+    const void* x;            /* dispatch: [tokens][cols], ld_tokens */
+    const int32_t* rows;
+    int64_t tokens;
+    int64_t cols;
+    int64_t row_count;
+    int64_t ld_tokens;        /* leading dimension of x / residual */
+    int64_t ld_rows;          /* leading dimension of values / y */
+    int32_t k;
+    int32_t dtype;
+    int32_t elem_format;
+    int32_t scale_mode;
+    float scale_factor;
+    void* values;
+    uint8_t* codes;
+    uint8_t* scales;
+    const void* y;            /* combine: [row_count][cols], ld_rows */
+    const float* weights;
+    const void* residual;     /* [tokens][cols], ld_tokens */
+    void* out;                /* [tokens][cols], ld_out */
+    int64_t ld_out;
+    const void* grad_out;     /* combine_bwd: [tokens][cols], ld_out */
+    void* grad_rows;
+    int64_t ld_grad_rows;
+    float* grad_weights;
+} mxfp4_moe_move_args;
+
+mxfp4_status mxfp4_moe_dispatch(const mxfp4_moe_move_args* args, mxfp4_stream_t stream);
+mxfp4_status mxfp4_moe_combine(const mxfp4_moe_move_args* args, mxfp4_stream_t stream);
+mxfp4_status mxfp4_moe_combine_bwd(const mxfp4_moe_move_args* args, mxfp4_stream_t stream);
+
+/* Activations of the grouped linear. SWIGLU is gated: columns 2j (gate) and
+ * 2j + 1 (up) of the pre-activation give column j = silu(gate) * up, so that
+ * the rows of a weight hold gate and up rows alternately. */
+#define MXFP4_ACT_NONE 0
+#define MXFP4_ACT_RELU 1
+#define MXFP4_ACT_GELU 2      /* z/2 (1 + erf(z / sqrt 2)) */
+#define MXFP4_ACT_GELU_TANH 3 /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+#define MXFP4_ACT_SILU 4      /* z / (1 + exp(-z)) */
+#define MXFP4_ACT_SWIGLU 5
+
+/*
+ * Grouped block-scaled product with its epilogue:
+ *   z = A B_g^T + bias_g,  y = act(z) + residual
+ * for the rows of A that the group list gives to group g; operands as in
+ * mxfp4_grouped_gemm with MXFP4_GMM_GROUP_M, accumulated, biased and activated
+ * in fp32, rounded once per output. The groups may end before row m: rows
+ * behind the last group are left as they were.
+ *   k           a positive multiple of 64 (E2M1) or 32 (E4M3); scale padding
+ *               behind the last block is not read as a scale.
+ *   a, lda, b, ldb  code rows, strides in bytes (multiples of 16), 16-byte
+ *               aligned; a_scales 4-byte, b_scales 16-byte aligned; group g's
+ *               scales at b_scales + g * mxfp4_scales_row_bytes(n, k, 32,
+ *               MXFP4_SCALES_MMA).
+ *   group_list  device int64[num_groups], or NULL for one group of all m
+ *               rows (num_groups is then ignored).
+ *   bias        optional fp32 [groups][n].
+ *   residual    optional, [m][n'] with n' = n (SWIGLU: n / 2), leading
+ *               dimension ld_res, d_dtype.
+ *   y           [m][n'], leading dimension ld_y; d_dtype MXFP4_F32 / MXFP4_BF16.
+ *   preact      optional, [m][n], leading dimension ld_preact: z in d_dtype.
+ *   status      optional device int32: MXFP4_EINVAL for a group list that is
+ *               not non-negative with a total of at most m (nothing is written).
+ *
+ * mxfp4_grouped_linear_bwd: from grad_out [m][n'] (ld_y) and the stored
+ * preact [m][n], grad_preact [m][n] (ld_grad; d_dtype; gated: d gate = grad up
+ * silu'(gate), d up = grad silu(gate)) and, optionally, grad_bias fp32
+ * [groups][n], the sums of the unrounded grad_preact over each group's rows
+ * (0 for an empty group). The residual's gradient is grad_out; the
+ * operands' gradients are grouped GEMMs of grad_preact. workspace:
+ * mxfp4_grouped_linear_workspace(m, n, num_groups) bytes, 4-byte aligned,
+ * when grad_bias is given. a, b and k are not used. Rows behind the last group
+ * are left as they were.
+ */
+typedef struct mxfp4_linear_args {
+    int32_t elem_format;
+    int32_t activation;
+    int64_t m, n, k;
+    const uint8_t* a;
+    int64_t lda;
+    const uint8_t* a_scales;
+    const uint8_t* b;
+    int64_t ldb;
+    const uint8_t* b_scales;
+    const int64_t* group_list;
+    int64_t num_groups;
+    int32_t group_list_type;
+    int32_t d_dtype;
+    const float* bias;
+    const void* residual;
+    int64_t ld_res;
+    void* y;
+    int64_t ld_y;
+    void* preact;
+    int64_t ld_preact;
+    int32_t* status;
+    const void* grad_out;
+    void* grad_preact;
+    int64_t ld_grad;
+    float* grad_bias;
+    void* workspace;
+    int64_t workspace_bytes;
+} mxfp4_linear_args;
+
+mxfp4_status mxfp4_grouped_linear(const mxfp4_linear_args* args, mxfp4_stream_t stream);
+int64_t mxfp4_grouped_linear_workspace(int64_t m, int64_t n, int64_t num_groups);
+mxfp4_status mxfp4_grouped_linear_bwd(const mxfp4_linear_args* args, mxfp4_stream_t stream);
 
 /* Static English text of a status; never NULL. */
 const char* mxfp4_status_string(mxfp4_status status);

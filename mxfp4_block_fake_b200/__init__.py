@@ -10,11 +10,22 @@ Layers:
 """
 from ._abi import MXFP4ArgumentError, MXFP4Error
 from .ops import (
+    DispatchResult,
     DualLevelResult,
+    LinearResult,
     QDQResult,
+    RouteResult,
     colwise_scale_rows_bound,
     mxfp4_colwise_scale_rows,
     mxfp4_dual_level_qdq,
+    mxfp4_grouped_gemm,
+    mxfp4_grouped_linear,
+    mxfp4_grouped_linear_bwd,
+    mxfp4_moe_combine,
+    mxfp4_moe_combine_bwd,
+    mxfp4_moe_dispatch,
+    mxfp4_moe_route,
+    mxfp4_moe_route_bwd,
     mxfp4_qdq_fwd,
     mxfp4_qdq_fwd_bwd,
     mxfp4_ste_bwd,
@@ -34,5 +45,7 @@ __all__ = [
     "MXFP4Error", "MXFP4ArgumentError", "QDQResult", "DualLevelResult", "mxfp4_dual_level_qdq", "colwise_scale_rows_bound", "mxfp4_colwise_scale_rows",
     "mxfp4_qdq_fwd", "mxfp4_qdq_fwd_bwd", "mxfp4_ste_bwd", "MXFP4FakeQuantizer", "MXFP4QATConfig",
     "MXFP4QATLinear", "convert_to_mxfp4_qat", "mxfp4_fake_quant", "mxfp4_quant_dequant",
-    "mxfp4_saturation_mask", "unpack_mask",
+    "mxfp4_saturation_mask", "unpack_mask", "DispatchResult", "LinearResult", "RouteResult", "mxfp4_grouped_gemm",
+    "mxfp4_grouped_linear", "mxfp4_grouped_linear_bwd", "mxfp4_moe_combine", "mxfp4_moe_combine_bwd",
+    "mxfp4_moe_dispatch", "mxfp4_moe_route", "mxfp4_moe_route_bwd",
 ]

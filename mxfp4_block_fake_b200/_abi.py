@@ -21,7 +21,10 @@ SCALES_ROWMAJOR, SCALES_MMA = 0, 1
 COLS_ROWMAJOR, COLS_MMA = 0, 1
 ELEM_E2M1, ELEM_E4M3 = 0, 1
 MAX_GROUPS = 4096
-ABI_VERSION = 5
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+GROUP_BEST, GROUP_TOP2 = 0, 1
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU, ACT_SWIGLU = range(6)
+ABI_VERSION = 6
 
 # Every symbol include/mxfp4.h declares.
 EXPORTS = (
@@ -36,6 +39,15 @@ EXPORTS = (
     "mxfp4_colwise_operand_scale_bytes",
     "mxfp4_grouped_gemm",
     "mxfp4_dual_level_qdq",
+    "mxfp4_moe_route_workspace",
+    "mxfp4_moe_route",
+    "mxfp4_moe_route_bwd",
+    "mxfp4_moe_dispatch",
+    "mxfp4_moe_combine",
+    "mxfp4_moe_combine_bwd",
+    "mxfp4_grouped_linear",
+    "mxfp4_grouped_linear_workspace",
+    "mxfp4_grouped_linear_bwd",
     "mxfp4_status_string",
     "mxfp4_abi_version",
 )
@@ -118,6 +130,98 @@ class DualLevelArgs(ctypes.Structure):
     ]
 
 
+class RouteArgs(ctypes.Structure):
+    _fields_ = [
+        ("logits", ctypes.c_void_p),
+        ("tokens", ctypes.c_int64),
+        ("experts", ctypes.c_int64),
+        ("ld", ctypes.c_int64),
+        ("dtype", ctypes.c_int32),
+        ("k", ctypes.c_int32),
+        ("score", ctypes.c_int32),
+        ("renormalize", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("num_groups", ctypes.c_int32),
+        ("topk_groups", ctypes.c_int32),
+        ("group_score", ctypes.c_int32),
+        ("bias", ctypes.c_void_p),
+        ("token_mask", ctypes.c_void_p),
+        ("weights", ctypes.c_void_p),
+        ("chosen", ctypes.c_void_p),
+        ("rows", ctypes.c_void_p),
+        ("slots", ctypes.c_void_p),
+        ("counts", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_int64),
+        ("grad_weights", ctypes.c_void_p),
+        ("grad_logits", ctypes.c_void_p),
+        ("ld_grad", ctypes.c_int64),
+    ]
+
+
+class MoveArgs(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p),
+        ("rows", ctypes.c_void_p),
+        ("tokens", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("row_count", ctypes.c_int64),
+        ("ld_tokens", ctypes.c_int64),
+        ("ld_rows", ctypes.c_int64),
+        ("k", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+        ("elem_format", ctypes.c_int32),
+        ("scale_mode", ctypes.c_int32),
+        ("scale_factor", ctypes.c_float),
+        ("values", ctypes.c_void_p),
+        ("codes", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
+        ("y", ctypes.c_void_p),
+        ("weights", ctypes.c_void_p),
+        ("residual", ctypes.c_void_p),
+        ("out", ctypes.c_void_p),
+        ("ld_out", ctypes.c_int64),
+        ("grad_out", ctypes.c_void_p),
+        ("grad_rows", ctypes.c_void_p),
+        ("ld_grad_rows", ctypes.c_int64),
+        ("grad_weights", ctypes.c_void_p),
+    ]
+
+
+class LinearArgs(ctypes.Structure):
+    _fields_ = [
+        ("elem_format", ctypes.c_int32),
+        ("activation", ctypes.c_int32),
+        ("m", ctypes.c_int64),
+        ("n", ctypes.c_int64),
+        ("k", ctypes.c_int64),
+        ("a", ctypes.c_void_p),
+        ("lda", ctypes.c_int64),
+        ("a_scales", ctypes.c_void_p),
+        ("b", ctypes.c_void_p),
+        ("ldb", ctypes.c_int64),
+        ("b_scales", ctypes.c_void_p),
+        ("group_list", ctypes.c_void_p),
+        ("num_groups", ctypes.c_int64),
+        ("group_list_type", ctypes.c_int32),
+        ("d_dtype", ctypes.c_int32),
+        ("bias", ctypes.c_void_p),
+        ("residual", ctypes.c_void_p),
+        ("ld_res", ctypes.c_int64),
+        ("y", ctypes.c_void_p),
+        ("ld_y", ctypes.c_int64),
+        ("preact", ctypes.c_void_p),
+        ("ld_preact", ctypes.c_int64),
+        ("status", ctypes.c_void_p),
+        ("grad_out", ctypes.c_void_p),
+        ("grad_preact", ctypes.c_void_p),
+        ("ld_grad", ctypes.c_int64),
+        ("grad_bias", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_int64),
+    ]
+
+
 class MXFP4Error(RuntimeError):
     """A libmxfp4 call returned a non-OK status."""
 
@@ -167,6 +271,16 @@ def lib() -> ctypes.CDLL:
     L.mxfp4_grouped_gemm.restype = i32
     L.mxfp4_dual_level_qdq.argtypes = [ctypes.POINTER(DualLevelArgs), P]
     L.mxfp4_dual_level_qdq.restype = i32
+    L.mxfp4_moe_route_workspace.argtypes = [i64, i64]
+    L.mxfp4_moe_route_workspace.restype = i64
+    L.mxfp4_grouped_linear_workspace.argtypes = [i64, i64, i64]
+    L.mxfp4_grouped_linear_workspace.restype = i64
+    for name, struct in (("mxfp4_moe_route", RouteArgs), ("mxfp4_moe_route_bwd", RouteArgs),
+                         ("mxfp4_moe_dispatch", MoveArgs), ("mxfp4_moe_combine", MoveArgs),
+                         ("mxfp4_moe_combine_bwd", MoveArgs), ("mxfp4_grouped_linear", LinearArgs),
+                         ("mxfp4_grouped_linear_bwd", LinearArgs)):
+        getattr(L, name).argtypes = [ctypes.POINTER(struct), P]
+        getattr(L, name).restype = i32
     L.mxfp4_status_string.argtypes = [i32]
     L.mxfp4_status_string.restype = ctypes.c_char_p
     L.mxfp4_abi_version.argtypes = []
@@ -233,3 +347,31 @@ def mxfp4_grouped_gemm(args: GmmArgs, stream: int) -> int:
 
 def mxfp4_dual_level_qdq(args: DualLevelArgs, stream: int) -> int:
     return lib().mxfp4_dual_level_qdq(ctypes.byref(args), stream)
+
+
+def mxfp4_moe_route(args: RouteArgs, stream: int) -> int:
+    return lib().mxfp4_moe_route(ctypes.byref(args), stream)
+
+
+def mxfp4_moe_route_bwd(args: RouteArgs, stream: int) -> int:
+    return lib().mxfp4_moe_route_bwd(ctypes.byref(args), stream)
+
+
+def mxfp4_moe_dispatch(args: MoveArgs, stream: int) -> int:
+    return lib().mxfp4_moe_dispatch(ctypes.byref(args), stream)
+
+
+def mxfp4_moe_combine(args: MoveArgs, stream: int) -> int:
+    return lib().mxfp4_moe_combine(ctypes.byref(args), stream)
+
+
+def mxfp4_moe_combine_bwd(args: MoveArgs, stream: int) -> int:
+    return lib().mxfp4_moe_combine_bwd(ctypes.byref(args), stream)
+
+
+def mxfp4_grouped_linear(args: LinearArgs, stream: int) -> int:
+    return lib().mxfp4_grouped_linear(ctypes.byref(args), stream)
+
+
+def mxfp4_grouped_linear_bwd(args: LinearArgs, stream: int) -> int:
+    return lib().mxfp4_grouped_linear_bwd(ctypes.byref(args), stream)

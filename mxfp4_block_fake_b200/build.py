@@ -9,41 +9,65 @@ travels with the source tree.
 from __future__ import annotations
 
 import os
+import re
 import subprocess
 import sys
+from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
-SRC = os.path.join(PKG, "csrc", "mxfp4.cu")
-HDR = os.path.join(ROOT, "include", "mxfp4.h")
+CSRC = os.path.join(PKG, "csrc")
+INCLUDE = os.path.join(ROOT, "include")
+SRCS = ("mxfp4.cu", "mxfp4_moe.cu")  # translation units, compiled side by side
+OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmxfp4.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",
-    "-Xcompiler", "-fPIC", "-shared",
+    "-Xcompiler", "-fPIC",
     "--expt-relaxed-constexpr",
     "-Xptxas", "-warn-spills",
 ]
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB):
-        return True
-    t = os.path.getmtime(LIB)
-    csrc = os.path.join(PKG, "csrc")
-    deps = (HDR, __file__, *(os.path.join(csrc, f) for f in os.listdir(csrc)))
-    return any(os.path.getmtime(p) > t for p in deps)
+def _sources(path: str, seen: set | None = None) -> set:
+    """path and every file of this tree it includes."""
+    seen = set() if seen is None else seen
+    if path not in seen:
+        seen.add(path)
+        with open(path) as f:
+            for name in re.findall(r'^#include "([^"]+)"', f.read(), re.M):
+                for d in (CSRC, INCLUDE):
+                    if os.path.exists(os.path.join(d, name)):
+                        _sources(os.path.join(d, name), seen)
+    return seen
+
+
+def _stale(out: str, deps) -> bool:
+    return not os.path.exists(out) or any(os.path.getmtime(p) > os.path.getmtime(out) for p in deps)
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    if not force and not verbose_ptxas and not _stale():
+    deps = {s: _sources(os.path.join(CSRC, s)) | {os.path.abspath(__file__)} for s in SRCS}
+    if not force and not verbose_ptxas and not _stale(LIB, set().union(*deps.values())):
         return LIB
-    cmd = [NVCC, *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-o", LIB + ".tmp", SRC]
-    if verbose_ptxas:
-        cmd[1:1] = ["-Xptxas", "-v"]
-    subprocess.run(cmd, check=True)
+    os.makedirs(OBJ, exist_ok=True)
+
+    def compile_one(src: str) -> str:
+        obj = os.path.join(OBJ, src + ".o")
+        if force or verbose_ptxas or _stale(obj, deps[src]):
+            cmd = [NVCC, *NVCC_FLAGS, "-I", INCLUDE, "-c", "-o", obj + ".tmp", os.path.join(CSRC, src)]
+            if verbose_ptxas:
+                cmd[1:1] = ["-Xptxas", "-v"]
+            subprocess.run(cmd, check=True)
+            os.replace(obj + ".tmp", obj)
+        return obj
+
+    with ThreadPoolExecutor(len(SRCS)) as pool:
+        objs = list(pool.map(compile_one, SRCS))
+    subprocess.run([NVCC, "-gencode", "arch=compute_100a,code=sm_100a", "-shared", "-o", LIB + ".tmp", *objs], check=True)
     os.replace(LIB + ".tmp", LIB)
     return LIB
 

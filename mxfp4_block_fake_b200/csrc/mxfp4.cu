@@ -25,186 +25,9 @@
 //  * generic kernels (one thread per block, scalar accesses) serve shapes and
 //    pointers the vector path cannot (cols or ld not a multiple of 16 bytes,
 //    unaligned buffers).
-#include <cuda.h>
-#include <cuda_runtime.h>
-
-#include <math.h>
-#include <stdint.h>
-#include <string.h>
-
-#include <mutex>
-
-#include "mxfp4.h"
+#include "mxfp4_common.cuh"
 
 namespace mxfp4 {
-
-constexpr unsigned FULL = 0xFFFFFFFFu;
-constexpr uint32_t QNAN32 = 0x7FC00000u;
-constexpr int NTHREADS = 256;
-
-struct KArgs {
-    const void* x;
-    int64_t rows, cols, ld;
-    float sf;
-    int32_t mode;
-    int32_t grad_dir;  // 0, MXFP4_ROWWISE or MXFP4_COLWISE
-    void* y_row;
-    void* y_col;
-    int64_t ld_y;
-    uint8_t* codes_row;
-    uint8_t* scales_row;
-    uint8_t* mask_row;
-    uint8_t* codes_col;
-    uint8_t* scales_col;
-    uint8_t* mask_col;
-    const void* g_out;
-    void* g_in;
-    int64_t ld_g;
-    const int64_t* group_list;
-    int32_t num_groups;
-    int32_t gl_type;
-    int32_t* status;
-    uint32_t n_ct;  // column tiles of the tile kernel
-    uint32_t thr;   // PAGE mode: fp32 bits of T0 (see qparams)
-    uint32_t ts_flags;  // staged kernel: column-wise outputs written by TMA stores (SG_TS_*)
-    int32_t srow_mma;   // scales_row in the MMA scale-factor layout (MXFP4_SCALES_MMA)
-    int32_t fmt;        // MXFP4_ELEM_E2M1 or MXFP4_ELEM_E4M3
-    int64_t k_alloc;    // column-wise operand layout: K slots per codes row (MXFP4_COLS_MMA)
-    // 4 and 65536, set by the host: the staged kernel scales table indices and
-    // moves halves with integer multiply-adds by these run-time values, which
-    // the compiler cannot turn back into shifts, so that this work runs on the
-    // multiply-add pipe beside the logic ops on the ALU pipe
-    uint32_t mul4, mul16;
-};
-
-// Byte offset of row-wise scale (row, b) of a [rows][nblk] scale matrix:
-// row-major, or the block-scaled MMA layout (atoms of 128 rows x 4 block
-// columns, 512 bytes, atom rows in order; entry (r, c) of an atom at
-// 16 (r mod 32) + 4 floor(r / 32) + c).
-__device__ __forceinline__ int64_t srow_off_mma(int64_t row, int64_t b, int64_t nblk)
-{
-    const int64_t ncb = (nblk + 3) >> 2;
-    return (((row >> 7) * ncb + (b >> 2)) << 9) + ((row & 31) << 4) + (((row >> 5) & 3) << 2) + (b & 3);
-}
-
-__device__ __forceinline__ int64_t srow_off(const KArgs& a, int64_t row, int64_t b, int64_t nblk)
-{
-    return a.srow_mma ? srow_off_mma(row, b, nblk) : row * nblk + b;
-}
-
-// ---------------------------------------------------------------------------
-// Per-block parameters
-// ---------------------------------------------------------------------------
-
-struct BP {
-    float inv;      // 2^-k
-    float scale;    // 2^k
-    uint32_t lim;   // fp32 bits of fl(6 * 2^k); +inf bits once it overflows
-    uint32_t nanm;  // all ones for a non-finite block
-    uint32_t e8;    // E8M0 byte
-};
-
-// fp32 bits of 2^k for k in [-127, 127] (2^-127 is the subnormal 0x00400000).
-__device__ __forceinline__ uint32_t pow2_bits(int k)
-{
-    return k >= -126 ? (uint32_t)(k + 127) << 23 : 0x00400000u;
-}
-
-// A = fp32 bits of the block's max |x| (integer max of sign-cleared bits, so a
-// NaN anywhere gives A > 0x7F800000 and an inf gives A == 0x7F800000).
-__device__ __forceinline__ BP block_params(uint32_t A, int mode, float sf)
-{
-    int k;
-    bool special = A >= 0x7F800000u;
-    if (mode == MXFP4_SCALE_FLOOR) {
-        // floor(log2 amax) - 2 from the biased exponent; subnormal and zero
-        // amax have a biased exponent of 0 and saturate at -127.
-        k = max((int)(A >> 23) - 129, -127);
-    } else {
-        // r = max(fl(amax / sf), 2^-30) is a normal fp32 number; round(log2 r)
-        // is its exponent plus one when its significand is at or above the
-        // first fp32 significand above sqrt(2) (1.0110101000001001111001100..b;
-        // fraction field 0x3504F3 < frac(sqrt 2) < 0x3504F4).
-        float r = fmaxf(__fdiv_rn(__uint_as_float(A), sf), 0x1p-30f);
-        uint32_t rb = __float_as_uint(r);
-        k = (int)(rb >> 23) - 127 + ((rb & 0x7FFFFFu) >= 0x3504F4u ? 1 : 0);
-        special = special || k > 127;  // 2^128 overflows fp32: scale = inf
-    }
-    if (special)
-        k = 0;
-    BP p;
-    p.inv = __uint_as_float(pow2_bits(-k));
-    p.scale = __uint_as_float(pow2_bits(k));
-    p.lim = k >= 126 ? 0x7F800000u : (((uint32_t)(k + 129) << 23) | 0x00400000u);
-    p.nanm = special ? 0xFFFFFFFFu : 0u;
-    p.e8 = special ? 0xFFu : (uint32_t)(k + 127);
-    return p;
-}
-
-// One element: returns the fp32 bits of sign(y) * code * 2^k with y = x * 2^-k
-// (== fl(x / 2^k)), and the E2M1 nibble and saturation flag.
-__device__ __forceinline__ uint32_t qdq_elem(uint32_t xb, const BP& p, uint32_t& nib, uint32_t& sat)
-{
-    const float y = __fmul_rn(__uint_as_float(xb), p.inv);
-    const float a = fabsf(y);
-    const uint32_t i = (uint32_t)(a >= 0.25f) + (uint32_t)(a >= 0.75f) + (uint32_t)(a >= 1.25f) +
-                       (uint32_t)(a >= 1.75f) + (uint32_t)(a >= 2.5f) + (uint32_t)(a >= 3.5f) +
-                       (uint32_t)(a >= 5.0f);
-    // code magnitude as fp32 bits: 0, 0.5, then (i << 22) + 0x3F000000 gives
-    // 1, 1.5, 2, 3, 4, 6 for i = 2..7 (two significant bits per binade)
-    const uint32_t cb = i >= 2u ? (i << 22) + 0x3F000000u : (i == 1u ? 0x3F000000u : 0u);
-    const uint32_t neg = y < 0.0f ? 0x80000000u : 0u;  // sign(-0) and sign(+0) are 0
-    const float o = __fmul_rn(__uint_as_float(cb | neg), p.scale);
-    nib = (neg >> 28) | i;
-    sat = (xb & 0x7FFFFFFFu) > p.lim ? 1u : 0u;
-    return __float_as_uint(o);
-}
-
-// ---------------------------------------------------------------------------
-// MXFP8: E4M3 elements (scale mode FLOOR, block 32)
-// ---------------------------------------------------------------------------
-
-// k = floor(log2 amax) - 8 from the biased exponent (E4M3's largest normal is
-// 1.75 * 2^8 = 448), saturated at -127 (subnormal and zero amax included).
-__device__ __forceinline__ int k_e4m3(uint32_t A) { return max((int)(A >> 23) - 135, -127); }
-
-__device__ __forceinline__ BP block_params8(uint32_t A)
-{
-    const bool special = A >= 0x7F800000u;
-    const int k = special ? 0 : k_e4m3(A);
-    BP p;
-    p.inv = __uint_as_float(pow2_bits(-k));
-    p.scale = __uint_as_float(pow2_bits(k));
-    p.lim = ((uint32_t)(k + 135) << 23) | 0x00600000u;  // fp32 bits of 448 * 2^k = 1.75 * 2^(k + 8)
-    p.nanm = special ? 0xFFFFFFFFu : 0u;
-    p.e8 = special ? 0xFFu : (uint32_t)(k + 127);
-    return p;
-}
-
-// One element: fp32 bits of decode(code) * 2^k (exact: codes have four
-// significant bits and 2^k >= 2^-127), the E4M3 code of y = x * 2^-k by the
-// hardware convert (nearest even, saturating at 448, sign kept) and the
-// saturation flag.
-__device__ __forceinline__ uint32_t qdq8_elem(uint32_t xb, const BP& p, uint32_t& code, uint32_t& sat)
-{
-    const float y = __fmul_rn(__uint_as_float(xb), p.inv);
-    uint16_t q;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(q) : "f"(0.0f), "f"(y));
-    uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(q));
-    float c;
-    asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %1;\n\tcvt.f32.f16 %0, l;\n\t}" : "=f"(c) : "r"(h));
-    code = q & 0xFFu;
-    sat = (xb & 0x7FFFFFFFu) > p.lim ? 1u : 0u;
-    return __float_as_uint(__fmul_rn(c, p.scale));
-}
-
-// fp32 bits -> the same bits rounded to bf16 (nearest even) in the top half;
-// finite values only.
-__device__ __forceinline__ uint32_t round_bf16_bits(uint32_t b)
-{
-    return (b + 0x7FFFu + ((b >> 16) & 1u)) & 0xFFFF0000u;
-}
 
 // ---------------------------------------------------------------------------
 // 16-byte vectors
@@ -265,102 +88,6 @@ struct Vec<4> {  // fp32 x 4
                           (m & 8u) ? 0u : g.w);
     }
 };
-
-__device__ __forceinline__ uint4 ld_stream(const void* p)
-{
-    uint4 r;
-    asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-        : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-        : "l"(p));
-    return r;
-}
-
-__device__ __forceinline__ void st_stream(void* p, const uint4& v)
-{
-    __stcs(reinterpret_cast<uint4*>(p), v);
-}
-
-// ---------------------------------------------------------------------------
-// group_list plan, built by every CTA in shared memory
-// ---------------------------------------------------------------------------
-
-// Writes s_rst[g] = sum_{j<g} n_j and s_bpre[g] = sum_{j<g} ceil(n_j / BS) for
-// g = 0..G and returns S = s_bpre[G], or -1 when the list is not a partition
-// of [0, rows): a negative count, a decreasing offset, or a wrong total.
-// Every thread of the CTA must call it; the first NTHREADS hold the groups.
-template <int BS>
-__device__ int64_t build_plan(const KArgs& a, int32_t* s_bpre, int32_t* s_rst)
-{
-    __shared__ long long s_wr[NTHREADS / 32], s_wb[NTHREADS / 32];
-    __shared__ int s_bad;
-    const int G = a.num_groups;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int per = (G + NTHREADS - 1) / NTHREADS;
-    const int g0 = min(G, tid * per), g1 = min(G, g0 + per);
-    if (tid == 0)
-        s_bad = 0;
-    __syncthreads();
-
-    long long lr = 0, lb = 0;
-    bool bad = false;
-    long long prev = (a.gl_type == 0 && g0 > 0) ? (long long)a.group_list[g0 - 1] : 0;
-    for (int g = g0; g < g1; ++g) {
-        long long v = a.group_list[g];
-        long long n = a.gl_type == 1 ? v : v - prev;
-        prev = v;
-        if (n < 0 || n > a.rows) {
-            bad = true;
-            n = 0;
-        }
-        lr += n;
-        lb += (n + BS - 1) / BS;
-    }
-    long long ir = lr, ib = lb;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        long long tr = __shfl_up_sync(FULL, ir, o);
-        long long tb = __shfl_up_sync(FULL, ib, o);
-        if (lane >= o) {
-            ir += tr;
-            ib += tb;
-        }
-    }
-    if (lane == 31 && warp < NTHREADS / 32) {  // a CTA may carry extra warps: they hold no groups
-        s_wr[warp] = ir;
-        s_wb[warp] = ib;
-    }
-    if (bad)
-        atomicOr(&s_bad, 1);
-    __syncthreads();
-    long long er = ir - lr, eb = ib - lb, tot_r = 0, tot_b = 0;
-    for (int w = 0; w < NTHREADS / 32; ++w) {
-        if (w < warp) {
-            er += s_wr[w];
-            eb += s_wb[w];
-        }
-        tot_r += s_wr[w];
-        tot_b += s_wb[w];
-    }
-    prev = (a.gl_type == 0 && g0 > 0) ? (long long)a.group_list[g0 - 1] : 0;
-    for (int g = g0; g < g1; ++g) {
-        long long v = a.group_list[g];
-        long long n = a.gl_type == 1 ? v : v - prev;
-        prev = v;
-        if (n < 0 || n > a.rows)
-            n = 0;
-        s_rst[g] = (int32_t)er;
-        s_bpre[g] = (int32_t)eb;
-        er += n;
-        eb += (n + BS - 1) / BS;
-    }
-    if (tid == 0) {
-        s_rst[G] = (int32_t)tot_r;
-        s_bpre[G] = (int32_t)tot_b;
-    }
-    __syncthreads();
-    const bool ok = !s_bad && tot_r == a.rows;
-    return ok ? (int64_t)tot_b : -1;
-}
 
 // Row-block rb -> first row and row count, for a plan built by build_plan.
 __device__ __forceinline__ void plan_lookup(const int32_t* s_bpre, const int32_t* s_rst, int G,
@@ -1180,106 +907,6 @@ namespace mxfp4 {
 // Host side
 // ---------------------------------------------------------------------------
 
-struct DevInfo {
-    int sms = 0;
-};
-
-static std::mutex g_mu;
-
-static int device_sms()
-{
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess)
-        return -1;
-    static DevInfo info[64];
-    std::lock_guard<std::mutex> lk(g_mu);
-    if (dev < 0 || dev >= 64)
-        return -1;
-    if (info[dev].sms == 0) {
-        int n = 0;
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-            return -1;
-        info[dev].sms = n;
-    }
-    return info[dev].sms;
-}
-
-// Resident CTAs per SM of `fn` launched with `threads` per CTA, cached per
-// (device, kernel).
-static int occupancy(const void* fn, size_t smem, int threads = NTHREADS)
-{
-    struct Entry {
-        const void* fn;
-        int dev;
-        size_t smem;
-        int occ;
-    };
-    static Entry cache[512];
-    static int n = 0;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess)
-        return -1;
-    {
-        std::lock_guard<std::mutex> lk(g_mu);
-        for (int i = 0; i < n; ++i)
-            if (cache[i].fn == fn && cache[i].dev == dev && cache[i].smem == smem)
-                return cache[i].occ;
-    }
-    int occ = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, fn, threads, smem) != cudaSuccess)
-        return -1;
-    if (occ < 1)
-        occ = 1;
-    std::lock_guard<std::mutex> lk(g_mu);
-    if (n < 512)
-        cache[n++] = Entry{fn, dev, smem, occ};
-    return occ;
-}
-
-static inline bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
-
-static float f32_of(uint32_t u)
-{
-    float f;
-    memcpy(&f, &u, 4);
-    return f;
-}
-
-static uint32_t u32_of(float f)
-{
-    uint32_t u;
-    memcpy(&u, &f, 4);
-    return u;
-}
-
-// PAGE-mode scale_factor range of the vector path: every threshold T0 * 2^j it
-// uses stays a normal fp32 number, and |x / 2^k| < 16 keeps floor(4|y|) inside
-// the 64-entry lookup table.
-static bool page_fast_ok(float sf) { return sf >= 0x1p-64f && sf <= 11.0f; }
-
-// T0 = the smallest fp32 a with fl(a / sf) >= C, C = 0x3FB504F4 (the first fp32
-// above sqrt 2), found by stepping from fl(C * sf) one ulp at a time with IEEE
-// fp32 host division (a -> fl(a / sf) is monotone).
-static uint32_t page_threshold(float sf)
-{
-    const float C = f32_of(0x3FB504F4u);
-    volatile float a = C * sf;
-    for (int i = 0; i < 64; ++i) {
-        volatile float prev = nextafterf(a, 0.0f);
-        volatile float q = prev / sf;
-        if (!(q >= C))
-            break;
-        a = prev;
-    }
-    for (int i = 0; i < 64; ++i) {
-        volatile float q = a / sf;
-        if (q >= C)
-            break;
-        a = nextafterf(a, INFINITY);
-    }
-    return u32_of(a);
-}
-
 typedef void (*KernelFn)(const KArgs);
 
 template <int ESZ, int BS, int LC, int RPT, int WR, bool GRAD>
@@ -1366,46 +993,6 @@ static mxfp4_status launch(KernelFn fn, int64_t work_units, size_t smem, const K
 }
 
 // ---- staged path: TMA tensor maps ------------------------------------------
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-// cuTensorMapEncodeTiled through the runtime's driver entry point (the library
-// does not link libcuda directly); nullptr when unavailable.
-static EncodeTiledFn encode_tiled()
-{
-    static EncodeTiledFn fn = nullptr;
-    static bool tried = false;
-    std::lock_guard<std::mutex> lk(g_mu);
-    if (!tried) {
-        tried = true;
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-        else
-            (void)cudaGetLastError();
-    }
-    return fn;
-}
-
-// One 2-D tiled map: inner dimension d0 (elements of esz bytes), outer d1,
-// row pitch bytes, box b0 x b1.
-static bool encode_2d(CUtensorMap* tm, CUtensorMapDataType dt, void* base, uint64_t d0, uint64_t d1, uint64_t pitch,
-                      uint32_t b0, uint32_t b1, CUtensorMapSwizzle sw)
-{
-    EncodeTiledFn fn = encode_tiled();
-    if (!fn)
-        return false;
-    const cuuint64_t dims[2] = {(cuuint64_t)d0, (cuuint64_t)d1};
-    const cuuint64_t strides[1] = {(cuuint64_t)pitch};
-    const cuuint32_t box[2] = {(cuuint32_t)b0, (cuuint32_t)b1};
-    const cuuint32_t estr[2] = {1, 1};
-    return fn(tm, dt, 2, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, sw,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 // Maps of the staged kernel. x: bf16 [rows, cols] with row pitch ld * 2
 // bytes, 64 x 32 boxes with the 128-byte swizzle (out-of-range elements read

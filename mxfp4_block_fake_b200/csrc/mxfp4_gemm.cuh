@@ -106,81 +106,12 @@ struct GmMaps {
     CUtensorMap a, b;     // A [a_rows][k bytes]; B [G * N or N][k bytes]
 };
 
-__device__ __forceinline__ uint64_t gm_smem_desc(uint32_t saddr, uint64_t layout, uint32_t sbo)
-{
-    // start address, leading byte offset 16 (unused by swizzled K-major
-    // layouts), stride byte offset between 8-row groups, descriptor version 1
-    // (sm_100), base offset 0, layout type in the top three bits
-    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) | ((uint64_t)((sbo >> 4) & 0x3FFFu) << 32) |
-           ((uint64_t)1 << 46) | (layout << 61);
-}
-
-// The 512-byte scale atom (32 rows of 16 bytes, no swizzle) as the source of
-// a tcgen05.cp 32x128b: core matrices of 8 rows x 16 bytes, 128 bytes apart.
-__device__ __forceinline__ uint64_t gm_sf_desc(uint32_t saddr)
-{
-    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
-}
-
 // Block-scaled instruction descriptor: E8M0 scales, K-major A and B, M = 128,
 // N = 128, the scale bytes sf_id of each 32-bit tensor-memory word.
 __device__ __forceinline__ uint32_t gm_idesc(uint32_t ab_fmt, uint32_t sf_id)
 {
     return (sf_id << 4) | (ab_fmt << 7) | (ab_fmt << 10) | ((uint32_t)(GM_BN >> 3) << 17) | (1u << 23) |
            ((uint32_t)(GM_BM >> 4) << 24) | (sf_id << 29);
-}
-
-template <int FMT>
-__device__ __forceinline__ void gm_mma(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                       uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t acc)
-{
-    if constexpr (FMT == MXFP4_ELEM_E2M1) {
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.block32 [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d_tmem),
-            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc), "r"(sfa_tmem), "r"(sfb_tmem)
-            : "memory");
-    } else {
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "setp.ne.b32 p, %4, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d_tmem),
-            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc), "r"(sfa_tmem), "r"(sfb_tmem)
-            : "memory");
-    }
-}
-
-__device__ __forceinline__ void gm_commit(uint32_t bar)
-{
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ void gm_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void gm_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-// 32 consecutive fp32 accumulator columns of this thread's tensor-memory lane.
-__device__ __forceinline__ void gm_ld32(uint32_t taddr, uint32_t (&v)[32])
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
-          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
-          "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
-          "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
-        : "r"(taddr));
-    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-
-// 2-D TMA load of a byte tile (box of 128 bytes x 128 rows, 128-byte
-// swizzle); the inner coordinate is a multiple of 64 bytes.
-__device__ __forceinline__ void gm_tma_load(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-        "l"(map), "r"(x), "r"(y), "r"(bar)
-        : "memory");
 }
 
 // Tile t of the CTA's sequence -> (group g, first row of A, A rows of the

@@ -1,0 +1,645 @@
+// mxfp4_linear.cuh -- the grouped block-scaled product with bias, activation
+// and residual in its epilogue, on the fifth-generation tensor cores, and the
+// epilogue's gradients (included by mxfp4_moe.cu; the definition is in
+// include/mxfp4.h, mxfp4_grouped_linear).
+//
+//   z[t][f] = sum_k decode(A[t][k]) 2^(sA-127) decode(B_g[f][k]) 2^(sB-127) + bias_g[f]
+//   y       = act(z) + residual
+//
+// Layout of the product: the features (rows of B_g, the expert's weight) are
+// the MMA's M side and the tokens its N side, so that a tile of few tokens
+// (decoding) costs few tensor-core columns instead of a padded 128-row tile,
+// the weight's scale atoms are copied as they lie in memory, the bias is one
+// value per thread of the epilogue, and a warp's store writes 32 consecutive
+// features of one token.
+//
+// One CTA per SM, persistent over tiles of 256 features (two M = 128 halves
+// that share the tokens' operand) x NT tokens:
+//   warp 0: producer. Per stage of 128-byte rows (256 E2M1 or 128 E4M3 K
+//     elements) the TMA loads of both halves and the tokens (128-byte
+//     swizzle), bulk copies of the weight's scale atoms, and asynchronous
+//     4-byte copies of the tokens' scales (a group's rows start anywhere in
+//     an atom).
+//   warp 1: copies the scale atoms into tensor memory (tcgen05.cp) and issues
+//     the block-scaled MMAs.
+//   warps 2-9: epilogue, four per half. A warp reads its 32 features of every
+//     token from tensor memory into registers, hands the accumulator back, and
+//     then does its arithmetic and stores while the next tile is multiplied.
+// Every wait on an mbarrier is bounded (SG_WAIT_NS); on expiry the CTA records
+// MXFP4_ECUDA, waits (bounded) for its loads and MMAs in flight, frees the
+// tensor memory and exits.
+
+namespace mxfp4 {
+
+constexpr int LN_FT = 256;              // features per tile
+constexpr int LN_THREADS = 320;         // producer, MMA, 8 epilogue warps
+constexpr uint32_t LN_TMEM_COLS = 512;
+constexpr int LN_ROW_BYTES = 128;       // bytes of an operand row per stage
+
+template <int FMT>
+struct LnFmt;
+template <>
+struct LnFmt<MXFP4_ELEM_E2M1> {
+    static constexpr int BK = 256;       // K elements per stage
+    static constexpr int ATOMS = 2;      // scale atoms (128 K) per stage
+    static constexpr int MMA_K = 64;
+    static constexpr uint32_t AB_FMT = 1;
+};
+template <>
+struct LnFmt<MXFP4_ELEM_E4M3> {
+    static constexpr int BK = 128;
+    static constexpr int ATOMS = 1;
+    static constexpr int MMA_K = 32;
+    static constexpr uint32_t AB_FMT = 0;
+};
+
+template <int FMT, int NT>
+struct __align__(1024) LnSmem {
+    static constexpr int ATOMS = LnFmt<FMT>::ATOMS;
+    static constexpr int S = 4;                    // stages (227 KB with the plan of MAX_GROUPS groups)
+    static constexpr int NACC = NT > 64 ? 1 : 2;   // accumulators in tensor memory
+    static constexpr uint32_t SF_COL0 = NACC * 2 * NT;
+    // groups whose plan (two words each) fits beside the stages
+    static constexpr int MAX_GROUPS = NT > 64 ? 2048 : MXFP4_MAX_GROUPS;
+    static_assert(SF_COL0 + S * 12 * ATOMS <= LN_TMEM_COLS, "tensor memory columns");
+    uint8_t w[S][LN_FT * LN_ROW_BYTES];
+    uint8_t x[S][NT * LN_ROW_BYTES];
+    uint8_t sfw[S][2][512 * ATOMS];
+    uint8_t sfx[S][512 * ATOMS];
+    unsigned long long full[S], empty[S], acc_full[2], acc_empty[2], done;
+    uint32_t tmem_base;
+    int err;
+};
+
+struct LnArgs {
+    const uint8_t* sfx;     // A's scales (tokens)
+    const uint8_t* sfw;     // B's scales, group g at g * sfw_group_bytes
+    const float* bias;      // [groups][n] or NULL
+    const void* residual;   // [m][ld_res] or NULL
+    void* y;                // [m][ld_y]
+    void* preact;           // [m][ld_z] or NULL
+    const int64_t* group_list;
+    int32_t* status;
+    int64_t m, n, k, ld_res, ld_y, ld_z, sfw_group_bytes;
+    int32_t num_groups, gl_type, act;
+};
+
+struct LnMaps {
+    CUtensorMap x, w;
+};
+
+struct LnTile {
+    int g, f0, nh;      // group, first feature, halves with features
+    int64_t row0;       // first token row
+    int rows;           // valid token rows (<= NT)
+};
+
+template <int NT>
+__device__ __forceinline__ LnTile ln_tile(const LnArgs& a, const int32_t* s_tpre, const int32_t* s_rst, int64_t t,
+                                          int n_ft)
+{
+    LnTile r;
+    const int mt = (int)(t / n_ft);
+    const int ft = (int)(t - (int64_t)mt * n_ft);
+    int lo = 0, hi = a.num_groups - 1;  // largest g with s_tpre[g] <= mt (skips empty groups)
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (s_tpre[mid] <= mt)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    r.g = lo;
+    r.row0 = (int64_t)s_rst[lo] + (int64_t)(mt - s_tpre[lo]) * NT;
+    r.rows = (int)min((int64_t)NT, (int64_t)s_rst[lo + 1] - r.row0);
+    r.f0 = ft * LN_FT;
+    r.nh = a.n - r.f0 > 128 ? 2 : 1;
+    return r;
+}
+
+__device__ __forceinline__ uint32_t ln_idesc(uint32_t ab_fmt, uint32_t sf_id, uint32_t n)
+{
+    return (sf_id << 4) | (ab_fmt << 7) | (ab_fmt << 10) | ((n >> 3) << 17) | (1u << 23) | ((128u >> 4) << 24) |
+           (sf_id << 29);
+}
+
+// Bytes of global memory (16-byte aligned, a multiple of 16) into shared memory.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+// The group plan in shared memory: s_tpre[g] = sum_{j<g} ceil(n_j / BS), s_rst[g]
+// = the group's first row. Without a group list all rows are one group.
+// Returns the number of row tiles, -1 for an invalid list. Contains __syncthreads.
+template <int BS, typename Args>
+__device__ int64_t ln_plan(const Args& a, int32_t* s_tpre, int32_t* s_rst)
+{
+    if (!a.group_list) {
+        const int64_t units = (a.m + BS - 1) / BS;
+        if (threadIdx.x == 0) {
+            s_tpre[0] = s_rst[0] = 0;
+            s_tpre[1] = (int32_t)units;
+            s_rst[1] = (int32_t)a.m;
+        }
+        __syncthreads();
+        return units;
+    }
+    KArgs pa;
+    memset(&pa, 0, sizeof(pa));
+    pa.group_list = a.group_list;
+    pa.num_groups = a.num_groups;
+    pa.gl_type = a.gl_type;
+    pa.rows = a.m;
+    return build_plan<BS, true>(pa, s_tpre, s_rst);
+}
+
+// ---- activations -----------------------------------------------------------
+
+__device__ __forceinline__ float act_sigmoid(float z) { return 1.0f / (1.0f + expf(-z)); }
+
+// act(z) of the elementwise activations. gelu_tanh: 0.5 z (1 + tanh u) is z
+// times the logistic function of 2u; gelu: 0.5 z erfc(-z / sqrt 2), which does
+// not cancel for negative z.
+__device__ __forceinline__ float act_value(float z, int act)
+{
+    switch (act) {
+    case MXFP4_ACT_RELU:
+        return z > 0.0f ? z : (z != z ? z : 0.0f);
+    case MXFP4_ACT_GELU:
+        return 0.5f * z * erfcf(-0.70710678118654752f * z);
+    case MXFP4_ACT_GELU_TANH:
+        return z * act_sigmoid(1.5957691216057308f * (z + 0.044715f * z * z * z));
+    case MXFP4_ACT_SILU:
+        return z * act_sigmoid(z);
+    default:
+        return z;
+    }
+}
+
+// d act / dz
+__device__ __forceinline__ float act_slope(float z, int act)
+{
+    switch (act) {
+    case MXFP4_ACT_RELU:
+        return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
+    case MXFP4_ACT_GELU:
+        return 0.5f * erfcf(-0.70710678118654752f * z) + z * 0.39894228040143268f * expf(-0.5f * z * z);
+    case MXFP4_ACT_GELU_TANH: {
+        if (fabsf(z) > 16.0f)  // saturated; z^2 must not overflow against a zero
+            return z > 0.0f ? 1.0f : 0.0f;
+        const float s = act_sigmoid(1.5957691216057308f * (z + 0.044715f * z * z * z));
+        return s + z * s * (1.0f - s) * 1.5957691216057308f * (1.0f + 0.134145f * z * z);
+    }
+    case MXFP4_ACT_SILU: {
+        const float s = act_sigmoid(z);
+        return s * (1.0f + z * (1.0f - s));
+    }
+    default:
+        return 1.0f;
+    }
+}
+
+template <bool F32>
+__device__ __forceinline__ float ln_load(const void* p, int64_t i)
+{
+    return F32 ? static_cast<const float*>(p)[i]
+               : __uint_as_float((uint32_t)static_cast<const uint16_t*>(p)[i] << 16);
+}
+
+template <bool F32>
+__device__ __forceinline__ void ln_store(void* p, int64_t i, float v)
+{
+    if constexpr (F32)
+        static_cast<float*>(p)[i] = v;
+    else
+        static_cast<uint16_t*>(p)[i] = (uint16_t)f32_to_bf16(v);
+}
+
+// 32 tokens of this thread's feature: v[i] = z of token row0 + i.
+template <bool F32>
+__device__ __forceinline__ void ln_epilogue32(const LnArgs& a, float (&v)[32], int64_t row0, int rows, int f, bool fok)
+{
+    if (a.preact && fok) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (i < rows)
+                ln_store<F32>(a.preact, (row0 + i) * a.ld_z + f, v[i]);
+    }
+    if (a.act == MXFP4_ACT_SWIGLU) {
+        // lanes 2j and 2j + 1 hold gate j and up j: of a pair of tokens the even
+        // lane finishes the first, the odd lane the second
+        const bool odd = threadIdx.x & 1;
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+            const float other = __shfl_xor_sync(FULL, odd ? v[i] : v[i + 1], 1);
+            const float gate = odd ? other : v[i], up = odd ? v[i + 1] : other;
+            float o = gate * act_sigmoid(gate) * up;
+            const int tok = i + (odd ? 1 : 0);
+            if (fok && tok < rows) {
+                if (a.residual)
+                    o += ln_load<F32>(a.residual, (row0 + tok) * a.ld_res + (f >> 1));
+                ln_store<F32>(a.y, (row0 + tok) * a.ld_y + (f >> 1), o);
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        if (fok && i < rows) {
+            float o = act_value(v[i], a.act);
+            if (a.residual)
+                o += ln_load<F32>(a.residual, (row0 + i) * a.ld_res + f);
+            ln_store<F32>(a.y, (row0 + i) * a.ld_y + f, o);
+        }
+    }
+}
+
+template <int FMT, int NT, bool F32>
+__global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_constant__ LnMaps maps, const LnArgs a)
+{
+    using F = LnFmt<FMT>;
+    using SM = LnSmem<FMT, NT>;
+    constexpr int S = SM::S, ATOMS = F::ATOMS, NACC = SM::NACC;
+    extern __shared__ __align__(1024) uint8_t ln_dyn[];
+    uint8_t* base = ln_dyn + ((1024u - (smem_addr(ln_dyn) & 1023u)) & 1023u);
+    SM& sm = *reinterpret_cast<SM*>(base);
+    int32_t* s_tpre = reinterpret_cast<int32_t*>(base + sizeof(SM));
+    int32_t* s_rst = s_tpre + a.num_groups + 1;
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) {
+        sm.err = 0;
+        for (int s = 0; s < S; ++s) {
+            mbar_init(smem_addr(&sm.full[s]), 1 + 32);  // the transactions + each producer lane's copies
+            mbar_init(smem_addr(&sm.empty[s]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_addr(&sm.acc_full[i]), 1);
+            mbar_init(smem_addr(&sm.acc_empty[i]), 8);
+        }
+        mbar_init(smem_addr(&sm.done), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&sm.tmem_base)),
+                     "r"(LN_TMEM_COLS)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        gm_fence_before();
+    }
+    const int64_t units = ln_plan<NT>(a, s_tpre, s_rst);  // contains __syncthreads
+    gm_fence_after();
+    const uint32_t tmem = sm.tmem_base;
+    if (blockIdx.x == 0 && tid == 0 && a.status)
+        *a.status = units >= 0 ? MXFP4_OK : MXFP4_EINVAL;
+
+    const int n_ft = (int)((a.n + LN_FT - 1) / LN_FT);
+    const int64_t tiles = units < 0 ? 0 : units * n_ft;
+    const int64_t nblk = a.k / 32, ncb = (nblk + 3) >> 2;
+    const int nmma = (int)(a.k / F::MMA_K);           // MMAs along K
+    const int nst = (int)((a.k + F::BK - 1) / F::BK);  // stages along K
+
+    if (warp == 0) {
+        // ---- producer
+        int s = 0;
+        uint32_t ph = 0, issued = 0;
+        for (int64_t t = blockIdx.x; t < tiles && !sm.err; t += gridDim.x) {
+            const LnTile tl = ln_tile<NT>(a, s_tpre, s_rst, t, n_ft);
+            const int wrow = (int)((int64_t)tl.g * a.n + tl.f0);
+            const uint8_t* sfw = a.sfw + tl.g * a.sfw_group_bytes + (int64_t)(tl.f0 >> 7) * ncb * 512;
+            const uint8_t* px[NT / 32];
+            uint32_t okx = 0;
+#pragma unroll
+            for (int q = 0; q < NT / 32; ++q) {
+                const int r = lane + 32 * q;
+                const bool ok = r < tl.rows;
+                px[q] = a.sfx + (ok ? srow_off_mma(tl.row0 + r, 0, nblk) : 0);
+                okx |= (ok ? 1u : 0u) << q;
+            }
+            for (int ks = 0; ks < nst; ++ks) {
+                if (!__all_sync(FULL, mbar_wait(smem_addr(&sm.empty[s]), ph ^ 1u))) {
+                    sm.err = 1;
+                    break;
+                }
+                const int na = (int)min((int64_t)ATOMS, ncb - (int64_t)ks * ATOMS);  // scale atoms of the stage
+                const uint32_t bar = smem_addr(&sm.full[s]);
+#pragma unroll
+                for (int i = 0; i < ATOMS; ++i) {
+                    const int64_t jo = ((int64_t)ks * ATOMS + i) * 512;
+                    const uint32_t dst = smem_addr(sm.sfx[s]) + 512 * i + 16 * lane;
+#pragma unroll
+                    for (int q = 0; q < NT / 32; ++q) {
+                        const bool ok = ((okx >> q) & 1u) && i < na;
+                        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + 4 * q),
+                                     "l"(px[q] + (ok ? jo : 0)), "r"(ok ? 4u : 0u)
+                                     : "memory");
+                    }
+                }
+                asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+                if (lane == 0) {
+                    mbar_expect_tx(bar, tl.nh * (128 * LN_ROW_BYTES + 512 * na) + NT * LN_ROW_BYTES);
+                    for (int h = 0; h < tl.nh; ++h) {
+                        gm_tma_load(smem_addr(sm.w[s]) + h * 128 * LN_ROW_BYTES, &maps.w, ks * LN_ROW_BYTES,
+                                    wrow + 128 * h, bar);
+                        bulk_load(smem_addr(sm.sfw[s][h]), sfw + ((int64_t)h * ncb + (int64_t)ks * ATOMS) * 512, 512 * na,
+                                  bar);
+                    }
+                    gm_tma_load(smem_addr(sm.x[s]), &maps.x, ks * LN_ROW_BYTES, (int)tl.row0, bar);
+                }
+                issued |= 1u << s;
+                if (++s == S) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+        }
+        // every load issued lands before the CTA leaves (the last load of stage
+        // i had the parity of its turn)
+        if (lane == 0)
+            for (int i = 0; i < S; ++i)
+                if (issued & (1u << i))
+                    (void)mbar_wait(smem_addr(&sm.full[i]), i < s ? ph : ph ^ 1u);
+        __syncwarp();
+    } else if (warp == 1) {
+        // ---- MMA issuer (lane 0)
+        if (lane == 0) {
+            int s = 0, acc = 0;
+            uint32_t ph = 0, aph = 0;
+            for (int64_t t = blockIdx.x; t < tiles && !sm.err; t += gridDim.x) {
+                const LnTile tl = ln_tile<NT>(a, s_tpre, s_rst, t, n_ft);
+                if (!mbar_wait(smem_addr(&sm.acc_empty[acc]), aph ^ 1u)) {
+                    sm.err = 1;
+                    break;
+                }
+                gm_fence_after();
+                const uint32_t d_tmem = tmem + (uint32_t)(acc * 2 * NT);
+                for (int ks = 0; ks < nst; ++ks) {
+                    if (!mbar_wait(smem_addr(&sm.full[s]), ph)) {
+                        sm.err = 1;
+                        break;
+                    }
+                    gm_fence_after();
+                    // the tokens' scales were written by the producer's copies
+                    // (generic proxy); tcgen05.cp reads them in the async proxy
+                    fence_async_smem();
+                    const uint32_t sf_col = tmem + SM::SF_COL0 + (uint32_t)(12 * ATOMS * s);
+                    const int na = (int)min((int64_t)ATOMS, ncb - (int64_t)ks * ATOMS);
+#pragma unroll
+                    for (int i = 0; i < ATOMS; ++i) {
+                        if (i >= na)
+                            break;
+                        for (int h = 0; h < tl.nh; ++h)
+                            asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(sf_col + 4u * (2 * i + h)),
+                                         "l"(gm_sf_desc(smem_addr(sm.sfw[s][h]) + 512 * i))
+                                         : "memory");
+                        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(sf_col + 4u * (2 * ATOMS + i)),
+                                     "l"(gm_sf_desc(smem_addr(sm.sfx[s]) + 512 * i))
+                                     : "memory");
+                    }
+                    const uint64_t wd = gm_smem_desc(smem_addr(sm.w[s]), 2, 1024);
+                    const uint64_t xd = gm_smem_desc(smem_addr(sm.x[s]), 2, 1024);
+                    const int nk = min(4, nmma - 4 * ks);
+                    for (int kk = 0; kk < nk; ++kk) {
+                        // 32 bytes of K per MMA; its first scale block is byte (block % 4) of atom (block / 4)
+                        const int blk = kk * (F::MMA_K / 32);
+                        const uint32_t ai = (uint32_t)(blk >> 2);
+                        const uint32_t id = ln_idesc(F::AB_FMT, (uint32_t)(blk & 3), NT);
+                        for (int h = 0; h < tl.nh; ++h)
+                            gm_mma<FMT>(d_tmem + h * NT, wd + (uint64_t)(h * 128 * LN_ROW_BYTES / 16) + 2u * kk, xd + 2u * kk, id,
+                                        sf_col + 4u * (2 * ai + h), sf_col + 4u * (2 * ATOMS + ai), (ks > 0 || kk > 0) ? 1u : 0u);
+                    }
+                    gm_commit(smem_addr(&sm.empty[s]));
+                    if (++s == S) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+                gm_commit(smem_addr(&sm.acc_full[acc]));
+                if (++acc == NACC) {
+                    acc = 0;
+                    aph ^= 1u;
+                }
+            }
+            // every MMA issued has completed before the tensor memory is freed
+            gm_commit(smem_addr(&sm.done));
+            (void)mbar_wait(smem_addr(&sm.done), 0);
+        }
+        __syncwarp();
+    } else {
+        // ---- epilogue: tensor-memory lanes 32 (warp % 4) .. + 31 of half h
+        const int quad = warp & 3, h = (warp - 2) >> 2;
+        int acc = 0;
+        uint32_t aph = 0;
+        for (int64_t t = blockIdx.x; t < tiles && !sm.err; t += gridDim.x) {
+            const LnTile tl = ln_tile<NT>(a, s_tpre, s_rst, t, n_ft);
+            const int f = tl.f0 + 128 * h + 32 * quad + lane;
+            const bool fok = f < a.n;
+            const float bias = a.bias && fok ? a.bias[(int64_t)tl.g * a.n + f] : 0.0f;
+            if (!__all_sync(FULL, mbar_wait(smem_addr(&sm.acc_full[acc]), aph))) {
+                sm.err = 1;
+                break;
+            }
+            gm_fence_after();
+            float v[NT / 32][32];
+#pragma unroll
+            for (int c = 0; c < NT / 32; ++c) {
+                uint32_t u[32];
+                __syncwarp();
+                gm_ld32(tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)(acc * 2 * NT + h * NT + 32 * c), u);
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    v[c][i] = __uint_as_float(u[i]) + bias;
+            }
+            gm_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(smem_addr(&sm.acc_empty[acc]));
+            if (++acc == NACC) {
+                acc = 0;
+                aph ^= 1u;
+            }
+            if (h < tl.nh) {
+#pragma unroll 1
+                for (int c = 0; c < NT / 32; ++c) {
+                    if (32 * c >= tl.rows)
+                        break;
+                    ln_epilogue32<F32>(a, v[0], tl.row0 + 32 * c, tl.rows - 32 * c, f, fok);
+                    // the next 32 tokens move up, so that the code exists once
+#pragma unroll
+                    for (int d = 0; d + 1 < NT / 32; ++d)
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            v[d][i] = v[d + 1][i];
+                }
+            }
+        }
+    }
+
+    __syncthreads();
+    if (tid == 0 && sm.err && a.status)
+        *a.status = MXFP4_ECUDA;
+    if (warp == 1) {
+        gm_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(LN_TMEM_COLS) : "memory");
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Gradients of the epilogue: dz = dy act'(z) (gated: d gate = dy up silu'(gate),
+// d up = dy silu(gate)), dbias_g = the sum of dz over the group's rows, in
+// fp32 from the unrounded dz. A CTA takes LB_ROWS rows of one group by 32
+// threads' columns; partial sums go to ws[unit][n], and a second kernel adds a
+// group's units in order.
+// ---------------------------------------------------------------------------
+
+constexpr int LB_ROWS = 64;
+
+struct LnBwdArgs {
+    const void* grad;      // [m][ld_g]
+    const void* z;         // [m][ld_z]
+    void* grad_z;          // [m][ld_dz]
+    float* grad_bias;      // [groups][n] or NULL
+    float* ws;             // [units][n]
+    const int64_t* group_list;
+    int32_t* status;
+    int64_t m, n, ld_g, ld_z, ld_dz;
+    int32_t num_groups, gl_type, act;
+};
+
+template <int ESZ, bool VEC>
+__global__ void __launch_bounds__(NTHREADS) linear_bwd_kernel(const LnBwdArgs a)
+{
+    constexpr int PER = VEC ? 16 / ESZ : 2;   // columns of z per thread
+    constexpr int WARPS = NTHREADS / 32;
+    extern __shared__ __align__(16) int32_t lb_dyn[];
+    __shared__ float s_sum[WARPS][32 * PER];
+    int32_t* s_tpre = lb_dyn;
+    int32_t* s_rst = lb_dyn + a.num_groups + 1;
+    const int64_t units = ln_plan<LB_ROWS>(a, s_tpre, s_rst);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (blockIdx.x == 0 && tid == 0 && a.status)
+        *a.status = units >= 0 ? MXFP4_OK : MXFP4_EINVAL;
+    const int64_t n_ct = (a.n + 32 * PER - 1) / (32 * PER);
+    const bool gated = a.act == MXFP4_ACT_SWIGLU;
+    for (int64_t w = blockIdx.x; w < (units < 0 ? 0 : units * n_ct); w += gridDim.x) {
+        const uint32_t unit = (uint32_t)(w / n_ct);
+        const int64_t c = (w - (int64_t)unit * n_ct) * 32 * PER + lane * PER;
+        int lo = 0, hi = a.num_groups - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if ((uint32_t)s_tpre[mid] <= unit)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        const int64_t r0 = (int64_t)s_rst[lo] + (int64_t)(unit - (uint32_t)s_tpre[lo]) * LB_ROWS;
+        const int nr = (int)min((int64_t)LB_ROWS, (int64_t)s_rst[lo + 1] - r0);
+        float sum[PER];
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            sum[i] = 0.0f;
+        for (int r = warp; r < nr; r += WARPS) {
+            const int64_t row = r0 + r;
+            float z[PER], g[PER];
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                z[i] = g[i] = 0.0f;
+            if constexpr (VEC) {
+                if (c < a.n) {
+                    piece_load<ESZ, PER>(a.z, row * a.ld_z + c, z);
+                    if (!gated) {
+                        piece_load<ESZ, PER>(a.grad, row * a.ld_g + c, g);
+                    } else {
+                        const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const char*>(a.grad) + (row * a.ld_g + (c >> 1)) * ESZ);
+                        if constexpr (ESZ == 2) {
+                            g[0] = __uint_as_float(q.x << 16);
+                            g[1] = __uint_as_float(q.x & 0xFFFF0000u);
+                            g[2] = __uint_as_float(q.y << 16);
+                            g[3] = __uint_as_float(q.y & 0xFFFF0000u);
+                        } else {
+                            g[0] = __uint_as_float(q.x);
+                            g[1] = __uint_as_float(q.y);
+                        }
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < PER; ++i)
+                    if (c + i < a.n) {
+                        z[i] = ln_load<ESZ == 4>(a.z, row * a.ld_z + c + i);
+                        if (!gated)
+                            g[i] = ln_load<ESZ == 4>(a.grad, row * a.ld_g + c + i);
+                    }
+                if (gated && c < a.n)
+                    g[0] = ln_load<ESZ == 4>(a.grad, row * a.ld_g + (c >> 1));
+            }
+            float d[PER];
+            if (gated) {
+#pragma unroll
+                for (int i = 0; i < PER; i += 2) {
+                    const float gate = z[i], s = act_sigmoid(gate);
+                    d[i] = g[i / 2] * z[i + 1] * (s * (1.0f + gate * (1.0f - s)));
+                    d[i + 1] = g[i / 2] * (gate * s);
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < PER; ++i)
+                    d[i] = g[i] * act_slope(z[i], a.act);
+            }
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                sum[i] += d[i];
+            if constexpr (VEC) {
+                if (c < a.n)
+                    piece_store<ESZ, PER>(a.grad_z, row * a.ld_dz + c, d);
+            } else {
+#pragma unroll
+                for (int i = 0; i < PER; ++i)
+                    if (c + i < a.n)
+                        ln_store<ESZ == 4>(a.grad_z, row * a.ld_dz + c + i, d[i]);
+            }
+        }
+        if (a.grad_bias) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i)
+                s_sum[warp][lane * PER + i] = sum[i];
+            __syncthreads();
+            const int64_t c0 = (w - (int64_t)unit * n_ct) * 32 * PER;
+            for (int i = tid; i < 32 * PER; i += NTHREADS) {
+                float v = 0.0f;
+#pragma unroll
+                for (int q = 0; q < WARPS; ++q)
+                    v += s_sum[q][i];
+                if (c0 + i < a.n)
+                    a.ws[(int64_t)unit * a.n + c0 + i] = v;
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// grad_bias[g][c] = the sum of the group's units, in order. Grid: column
+// blocks x groups.
+__global__ void __launch_bounds__(NTHREADS) linear_bias_kernel(const LnBwdArgs a)
+{
+    extern __shared__ __align__(16) int32_t lb_dyn[];
+    int32_t* s_tpre = lb_dyn;
+    int32_t* s_rst = lb_dyn + a.num_groups + 1;
+    if (ln_plan<LB_ROWS>(a, s_tpre, s_rst) < 0)
+        return;
+    const int64_t c = (int64_t)blockIdx.x * NTHREADS + threadIdx.x;
+    if (c >= a.n)
+        return;
+    for (int g = blockIdx.y; g < a.num_groups; g += gridDim.y) {
+        float v = 0.0f;
+#pragma unroll 4
+        for (int u = s_tpre[g]; u < s_tpre[g + 1]; ++u)
+            v += a.ws[(int64_t)u * a.n + c];
+        a.grad_bias[(int64_t)g * a.n + c] = v;
+    }
+}
+
+}  // namespace mxfp4

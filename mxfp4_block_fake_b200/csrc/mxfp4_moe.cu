@@ -1,0 +1,533 @@
+// mxfp4_moe.cu -- the mixture-of-experts operators of libmxfp4.so: routing,
+// dispatch and combine, and the grouped block-scaled linear (include/mxfp4.h).
+#include "mxfp4_common.cuh"
+
+namespace mxfp4 {
+
+// fp32 -> bf16, nearest even.
+__device__ __forceinline__ uint32_t bf16x2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t f32_to_bf16(float v) { return bf16x2(v, 0.0f) & 0xFFFFu; }
+
+}  // namespace mxfp4
+
+#include "mxfp4_route.cuh"
+#include "mxfp4_permute.cuh"
+#include "mxfp4_linear.cuh"
+
+namespace mxfp4 {
+
+static mxfp4_status launched(cudaError_t e) { return e == cudaSuccess ? MXFP4_OK : MXFP4_ECUDA; }
+
+template <typename A>
+static mxfp4_status launch1(const void* fn, int64_t grid, int threads, size_t smem, const A& arg, cudaStream_t s)
+{
+    if (smem > 48 * 1024 && cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return MXFP4_ECUDA;
+    A a = arg;
+    void* args[] = {&a};
+    return launched(cudaLaunchKernel(fn, dim3((unsigned)grid), dim3((unsigned)threads), args, smem, s));
+}
+
+// Grid of a grid-stride kernel over `units` threads' work.
+static int64_t stride_grid(const void* fn, int64_t units)
+{
+    const int sms = device_sms(), occ = occupancy(fn, 0);
+    if (sms <= 0 || occ <= 0)
+        return -1;
+    const int64_t need = (units + NTHREADS - 1) / NTHREADS, most = (int64_t)sms * occ;
+    return need < most ? (need < 1 ? 1 : need) : most;
+}
+
+template <typename A>
+static mxfp4_status launch_stride(const void* fn, int64_t units, const A& a, cudaStream_t s)
+{
+    const int64_t grid = stride_grid(fn, units);
+    return grid < 0 ? MXFP4_ECUDA : launch1(fn, grid, NTHREADS, 0, a, s);
+}
+
+// ---- routing ---------------------------------------------------------------
+
+static int64_t route_chunks(int64_t tokens) { return tokens <= RT_CHUNK ? 1 : (tokens + RT_CHUNK - 1) / RT_CHUNK; }
+
+static mxfp4_status route_args(const mxfp4_moe_route_args* A, RouteArgs* r)
+{
+    if (!A)
+        return MXFP4_EINVAL;
+    if (A->dtype != MXFP4_F32 && A->dtype != MXFP4_BF16)
+        return MXFP4_EINVAL;
+    if (A->tokens < 0 || A->experts < 1 || A->k < 1 || A->k > A->experts || A->ld < A->experts)
+        return MXFP4_EINVAL;
+    if (A->score != MXFP4_SCORE_SOFTMAX && A->score != MXFP4_SCORE_SIGMOID)
+        return MXFP4_EINVAL;
+    if (!(A->scale == A->scale) || isinf(A->scale))
+        return MXFP4_EINVAL;
+    if (A->experts > RT_MAX_EXPERTS || A->k > RT_MAX_K || A->tokens > INT32_MAX / A->k)
+        return MXFP4_EUNSUPPORTED;
+    memset(r, 0, sizeof(*r));
+    r->logits = A->logits;
+    r->tokens = A->tokens;
+    r->ld = A->ld;
+    r->experts = (int32_t)A->experts;
+    r->k = A->k;
+    r->sigmoid = A->score == MXFP4_SCORE_SIGMOID;
+    r->renorm = A->renormalize != 0;
+    r->bf16 = A->dtype == MXFP4_BF16;
+    r->scale = A->scale;
+    r->experts_out = A->chosen;
+    return MXFP4_OK;
+}
+
+static mxfp4_status run_route(const mxfp4_moe_route_args* A, cudaStream_t s)
+{
+    RouteArgs r;
+    const mxfp4_status st = route_args(A, &r);
+    if (st != MXFP4_OK)
+        return st;
+    if (A->num_groups < 1 || A->experts % A->num_groups != 0 || A->topk_groups < 1 || A->topk_groups > A->num_groups)
+        return MXFP4_EINVAL;
+    if (A->group_score != MXFP4_GROUP_BEST && A->group_score != MXFP4_GROUP_TOP2)
+        return MXFP4_EINVAL;
+    if (A->k > A->topk_groups * (A->experts / A->num_groups))
+        return MXFP4_EINVAL;
+    if (A->num_groups > RT_MAX_GROUPS)
+        return MXFP4_EUNSUPPORTED;
+    if (!A->counts || (A->tokens > 0 && (!A->logits || !A->weights || !A->chosen || !A->rows || !A->slots)))
+        return MXFP4_EINVAL;
+    const size_t esz = A->dtype == MXFP4_BF16 ? 2 : 4;
+    if (!aligned(A->logits, esz) || !aligned(A->bias, 4) || !aligned(A->weights, 4) || !aligned(A->chosen, 4) ||
+        !aligned(A->rows, 4) || !aligned(A->slots, 4) || !aligned(A->counts, 8) || !aligned(A->workspace, 4))
+        return MXFP4_EINVAL;
+    const int64_t need = mxfp4_moe_route_workspace(A->tokens, A->experts);
+    if (need > 0 && (!A->workspace || A->workspace_bytes < need))
+        return MXFP4_EINVAL;
+    r.bias = A->bias;
+    r.token_mask = A->token_mask;
+    r.weights = A->weights;
+    r.rows = A->rows;
+    r.slots = A->slots;
+    r.counts = A->counts;
+    r.ws = static_cast<int32_t*>(A->workspace);
+    r.groups = A->num_groups;
+    r.topk_groups = A->topk_groups;
+    r.top2 = A->group_score == MXFP4_GROUP_TOP2;
+    r.chunks = (int32_t)route_chunks(A->tokens);
+    const size_t smem = (size_t)RT_WARPS * r.experts * 8 + (size_t)r.experts * 8 + (size_t)RT_CHUNK * r.k * 2;
+    mxfp4_status e = launch1((const void*)route_kernel, r.chunks, RT_THREADS, smem, r, s);
+    if (e == MXFP4_OK && r.chunks > 1)
+        e = launch1((const void*)route_scan_kernel, (r.experts + 31) / 32, 1024, 0, r, s);
+    if (e == MXFP4_OK && r.chunks > 1)
+        e = launch1((const void*)route_place_kernel, r.chunks, RT_THREADS, 0, r, s);
+    return e;
+}
+
+static mxfp4_status run_route_bwd(const mxfp4_moe_route_args* A, cudaStream_t s)
+{
+    RouteBwdArgs b;
+    const mxfp4_status st = route_args(A, &b.r);
+    if (st != MXFP4_OK)
+        return st;
+    if (A->ld_grad < A->experts)
+        return MXFP4_EINVAL;
+    if (A->tokens == 0)
+        return MXFP4_OK;
+    const size_t esz = A->dtype == MXFP4_BF16 ? 2 : 4;
+    if (!A->logits || !A->chosen || !A->grad_weights || !A->grad_logits || !aligned(A->logits, esz) ||
+        !aligned(A->chosen, 4) || !aligned(A->grad_weights, 4) || !aligned(A->grad_logits, esz))
+        return MXFP4_EINVAL;
+    b.grad_w = A->grad_weights;
+    b.grad_logits = A->grad_logits;
+    b.ld_g = A->ld_grad;
+    return launch1((const void*)route_bwd_kernel, (A->tokens + RT_WARPS - 1) / RT_WARPS, RT_THREADS,
+                   (size_t)RT_WARPS * A->experts * 4, b, s);
+}
+
+// ---- dispatch and combine --------------------------------------------------
+
+static mxfp4_status check_move(const mxfp4_moe_move_args* A)
+{
+    if (!A)
+        return MXFP4_EINVAL;
+    if (A->dtype != MXFP4_F32 && A->dtype != MXFP4_BF16)
+        return MXFP4_EINVAL;
+    if (A->tokens < 0 || A->cols < 0 || A->row_count < 0 || A->k < 1)
+        return MXFP4_EINVAL;
+    if (A->k > MXFP4_MOE_MAX_K || A->tokens > INT32_MAX / A->k || A->row_count > INT32_MAX || A->cols > INT32_MAX)
+        return MXFP4_EUNSUPPORTED;
+    if (A->tokens > 0 && (!A->rows || !aligned(A->rows, 4)))
+        return MXFP4_EINVAL;
+    return MXFP4_OK;
+}
+
+static size_t esize(const mxfp4_moe_move_args* A) { return A->dtype == MXFP4_BF16 ? 2 : 4; }
+
+// Whether rows of this pitch from this base are whole 16-byte vectors.
+static bool vec_rows(const void* p, int64_t ld, size_t esz) { return aligned(p, 16) && (ld * (int64_t)esz) % 16 == 0; }
+
+static mxfp4_status run_dispatch(const mxfp4_moe_move_args* A, cudaStream_t s)
+{
+    mxfp4_status st = check_move(A);
+    if (st != MXFP4_OK)
+        return st;
+    const size_t esz = esize(A);
+    const bool e4 = A->elem_format == MXFP4_ELEM_E4M3;
+    if (!A->values && !A->codes)
+        return MXFP4_EINVAL;
+    if (A->ld_tokens < A->cols || (A->values && A->ld_rows < A->cols))
+        return MXFP4_EINVAL;
+    if (A->codes) {
+        if (!A->scales || (A->elem_format != MXFP4_ELEM_E2M1 && !e4))
+            return MXFP4_EINVAL;
+        if (A->scale_mode != MXFP4_SCALE_PAGE && A->scale_mode != MXFP4_SCALE_FLOOR)
+            return MXFP4_EINVAL;
+        if (!(A->scale_factor > 0.0f) || isinf(A->scale_factor))
+            return MXFP4_EINVAL;
+        if (e4 && A->scale_mode != MXFP4_SCALE_FLOOR)
+            return MXFP4_EUNSUPPORTED;
+    }
+    if (A->cols == 0 || (A->tokens > 0 && A->row_count > 0 && (!A->x || !aligned(A->x, esz) || !aligned(A->values, esz))))
+        return A->cols == 0 ? MXFP4_OK : MXFP4_EINVAL;
+    DispatchArgs a;
+    memset(&a, 0, sizeof(a));
+    a.x = A->x;
+    a.rows = A->rows;
+    a.y = A->values;
+    a.codes = A->codes;
+    a.scales = A->scales;
+    a.tokens = A->tokens;
+    a.cols = A->cols;
+    a.ld = A->ld_tokens;
+    a.ld_y = A->ld_rows;
+    a.out_rows = A->row_count;
+    a.code_ld = e4 ? A->cols : (A->cols + 1) / 2;
+    a.sf = A->scale_factor;
+    a.k = A->k;
+    a.mode = A->scale_mode;
+    const bool work = A->tokens > 0 && A->row_count > 0;
+    if (A->values && work) {
+        const bool vec = vec_rows(A->x, A->ld_tokens, esz) && vec_rows(A->values, A->ld_rows, esz) &&
+                         (A->cols * esz) % 16 == 0;
+        const void* fn = esz == 2 ? (vec ? (const void*)dispatch_values_kernel<2, true> : (const void*)dispatch_values_kernel<2, false>)
+                                  : (vec ? (const void*)dispatch_values_kernel<4, true> : (const void*)dispatch_values_kernel<4, false>);
+        st = launch_stride(fn, A->tokens * (vec ? A->cols * (int64_t)esz / 16 : A->cols), a, s);
+    }
+    if (A->codes && st == MXFP4_OK) {
+        const int64_t npad = ((A->cols + 31) / 32 + 3) & ~(int64_t)3;
+        const void* fn = esz == 2 ? (e4 ? (const void*)dispatch_quant_kernel<2, MXFP4_ELEM_E4M3> : (const void*)dispatch_quant_kernel<2, MXFP4_ELEM_E2M1>)
+                                  : (e4 ? (const void*)dispatch_quant_kernel<4, MXFP4_ELEM_E4M3> : (const void*)dispatch_quant_kernel<4, MXFP4_ELEM_E2M1>);
+        if (work)
+            st = launch_stride(fn, A->tokens * npad, a, s);
+        if (st == MXFP4_OK && A->row_count % 128 != 0)
+            st = launch_stride((const void*)pad_scale_kernel, (128 - A->row_count % 128) * npad, a, s);
+    }
+    return st;
+}
+
+static void combine_args(const mxfp4_moe_move_args* A, CombineArgs* a)
+{
+    memset(a, 0, sizeof(*a));
+    a->y = A->y;
+    a->rows = A->rows;
+    a->weights = A->weights;
+    a->residual = A->residual;
+    a->out = A->out;
+    a->tokens = A->tokens;
+    a->cols = A->cols;
+    a->ld_y = A->ld_rows;
+    a->ld_res = A->ld_tokens;
+    a->ld_out = A->ld_out;
+    a->y_rows = A->row_count;
+    a->k = A->k;
+    a->grad = A->grad_out;
+    a->grad_y = A->grad_rows;
+    a->grad_w = A->grad_weights;
+    a->ld_gy = A->ld_grad_rows;
+}
+
+static mxfp4_status run_combine(const mxfp4_moe_move_args* A, cudaStream_t s)
+{
+    const mxfp4_status st = check_move(A);
+    if (st != MXFP4_OK)
+        return st;
+    const size_t esz = esize(A);
+    if (A->ld_out < A->cols || A->ld_rows < A->cols || (A->residual && A->ld_tokens < A->cols))
+        return MXFP4_EINVAL;
+    if (A->tokens == 0 || A->cols == 0)
+        return MXFP4_OK;
+    if (!A->out || (A->row_count > 0 && !A->y) || !aligned(A->y, esz) || !aligned(A->out, esz) ||
+        !aligned(A->residual, esz) || !aligned(A->weights, 4))
+        return MXFP4_EINVAL;
+    CombineArgs a;
+    combine_args(A, &a);
+    const bool vec = (A->cols * esz) % 16 == 0 && vec_rows(A->y, A->ld_rows, esz) && vec_rows(A->out, A->ld_out, esz) &&
+                     (!A->residual || vec_rows(A->residual, A->ld_tokens, esz));
+    const void* fn = esz == 2 ? (vec ? (const void*)combine_kernel<2, true> : (const void*)combine_kernel<2, false>)
+                              : (vec ? (const void*)combine_kernel<4, true> : (const void*)combine_kernel<4, false>);
+    return launch_stride(fn, A->tokens * (vec ? A->cols * (int64_t)esz / 16 : A->cols), a, s);
+}
+
+static mxfp4_status run_combine_bwd(const mxfp4_moe_move_args* A, cudaStream_t s)
+{
+    const mxfp4_status st = check_move(A);
+    if (st != MXFP4_OK)
+        return st;
+    const size_t esz = esize(A);
+    if (A->ld_out < A->cols || (A->grad_weights && A->ld_rows < A->cols) || (A->grad_rows && A->ld_grad_rows < A->cols))
+        return MXFP4_EINVAL;
+    if (!A->grad_rows && !A->grad_weights)
+        return MXFP4_EINVAL;
+    if (A->tokens == 0)
+        return MXFP4_OK;
+    if ((A->cols > 0 && !A->grad_out) || (A->grad_weights && A->row_count > 0 && A->cols > 0 && !A->y) ||
+        !aligned(A->grad_out, esz) || !aligned(A->y, esz) || !aligned(A->grad_rows, esz) || !aligned(A->weights, 4) ||
+        !aligned(A->grad_weights, 4))
+        return MXFP4_EINVAL;
+    CombineArgs a;
+    combine_args(A, &a);
+    const bool vec = (A->cols * esz) % 16 == 0 && vec_rows(A->grad_out, A->ld_out, esz) &&
+                     (!A->grad_weights || vec_rows(A->y, A->ld_rows, esz)) &&
+                     (!A->grad_rows || vec_rows(A->grad_rows, A->ld_grad_rows, esz));
+    const void* fn = esz == 2 ? (vec ? (const void*)combine_bwd_kernel<2, true> : (const void*)combine_bwd_kernel<2, false>)
+                              : (vec ? (const void*)combine_bwd_kernel<4, true> : (const void*)combine_bwd_kernel<4, false>);
+    return launch1(fn, A->tokens, NTHREADS, 0, a, s);
+}
+
+// ---- grouped linear --------------------------------------------------------
+
+template <int FMT, int NT, bool F32>
+static mxfp4_status launch_linear_t(const LnMaps& maps, const LnArgs& g, cudaStream_t s)
+{
+    using SM = LnSmem<FMT, NT>;
+    const void* fn = (const void*)linear_kernel<FMT, NT, F32>;
+    const size_t smem = sizeof(SM) + 1024 + (size_t)(2 * (g.num_groups + 1)) * sizeof(int32_t);
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return MXFP4_ECUDA;
+    const int sms = device_sms();
+    if (sms <= 0)
+        return MXFP4_ECUDA;
+    const int64_t bound = (g.m / NT + g.num_groups) * ((g.n + LN_FT - 1) / LN_FT);
+    LnMaps m = maps;
+    LnArgs a = g;
+    void* args[] = {&m, &a};
+    return launched(cudaLaunchKernel(fn, dim3((unsigned)(bound < sms ? bound : sms)), dim3(LN_THREADS), args, smem, s));
+}
+
+template <int FMT, int NT>
+static mxfp4_status launch_linear_n(const mxfp4_linear_args* A, LnMaps maps, const LnArgs& g, int64_t kb, bool f32, cudaStream_t s)
+{
+    if (!encode_2d(&maps.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t*>(A->a), (uint64_t)kb, (uint64_t)A->m,
+                   (uint64_t)A->lda, LN_ROW_BYTES, NT, CU_TENSOR_MAP_SWIZZLE_128B))
+        return MXFP4_ECUDA;
+    return f32 ? launch_linear_t<FMT, NT, true>(maps, g, s) : launch_linear_t<FMT, NT, false>(maps, g, s);
+}
+
+template <int FMT>
+static mxfp4_status launch_linear(const mxfp4_linear_args* A, const LnMaps& maps, const LnArgs& g, int64_t kb, bool f32, cudaStream_t s)
+{
+    // tokens per tile by the groups' mean size (their sizes are device data)
+    const int64_t mean = g.m / g.num_groups;
+    if (mean <= 32)
+        return launch_linear_n<FMT, 32>(A, maps, g, kb, f32, s);
+    if (mean <= 64 || g.num_groups > LnSmem<FMT, 128>::MAX_GROUPS)
+        return launch_linear_n<FMT, 64>(A, maps, g, kb, f32, s);
+    return launch_linear_n<FMT, 128>(A, maps, g, kb, f32, s);
+}
+
+static mxfp4_status check_linear(const mxfp4_linear_args* A)
+{
+    if (!A)
+        return MXFP4_EINVAL;
+    if (A->activation < MXFP4_ACT_NONE || A->activation > MXFP4_ACT_SWIGLU)
+        return MXFP4_EINVAL;
+    if (A->d_dtype != MXFP4_F32 && A->d_dtype != MXFP4_BF16)
+        return MXFP4_EINVAL;
+    if (A->m < 0 || A->n < 0 || (A->activation == MXFP4_ACT_SWIGLU && A->n % 2 != 0))
+        return MXFP4_EINVAL;
+    if (A->group_list && (A->num_groups < 1 || (A->group_list_type != 0 && A->group_list_type != 1) || !aligned(A->group_list, 8)))
+        return MXFP4_EINVAL;
+    if (A->m > INT32_MAX || A->n > INT32_MAX || (A->group_list && A->num_groups > MXFP4_MAX_GROUPS))
+        return MXFP4_EUNSUPPORTED;
+    return MXFP4_OK;
+}
+
+static mxfp4_status zero_status(int32_t* status, cudaStream_t s)
+{
+    return status ? launched(cudaMemsetAsync(status, 0, sizeof(int32_t), s)) : MXFP4_OK;
+}
+
+static mxfp4_status run_linear(const mxfp4_linear_args* A, cudaStream_t s)
+{
+    const mxfp4_status st = check_linear(A);
+    if (st != MXFP4_OK)
+        return st;
+    const bool e2 = A->elem_format == MXFP4_ELEM_E2M1, gated = A->activation == MXFP4_ACT_SWIGLU;
+    if (!e2 && A->elem_format != MXFP4_ELEM_E4M3)
+        return MXFP4_EINVAL;
+    if (A->k < 1 || A->k % (e2 ? 64 : 32) != 0)
+        return MXFP4_EINVAL;
+    if (A->k > INT32_MAX)
+        return MXFP4_EUNSUPPORTED;
+    const int64_t kb = e2 ? A->k / 2 : A->k, width = gated ? A->n / 2 : A->n;
+    const size_t esz = A->d_dtype == MXFP4_F32 ? 4 : 2;
+    if (A->ld_y < width || (A->residual && A->ld_res < width) || (A->preact && A->ld_preact < A->n))
+        return MXFP4_EINVAL;
+    if (A->m == 0 || A->n == 0)
+        return zero_status(A->status, s);
+    if (!A->a || !A->b || !A->a_scales || !A->b_scales || !A->y)
+        return MXFP4_EINVAL;
+    if (A->lda < kb || A->ldb < kb || A->lda % 16 != 0 || A->ldb % 16 != 0 || !aligned(A->a, 16) || !aligned(A->b, 16) ||
+        !aligned(A->a_scales, 4) || !aligned(A->b_scales, 16))
+        return MXFP4_EINVAL;
+    if (!aligned(A->y, esz) || !aligned(A->residual, esz) || !aligned(A->preact, esz) || !aligned(A->bias, 4) || !aligned(A->status, 4))
+        return MXFP4_EINVAL;
+    LnArgs g;
+    memset(&g, 0, sizeof(g));
+    g.num_groups = A->group_list ? (int32_t)A->num_groups : 1;
+    if (A->n * g.num_groups > INT32_MAX)
+        return MXFP4_EUNSUPPORTED;
+    g.sfx = A->a_scales;
+    g.sfw = A->b_scales;
+    g.bias = A->bias;
+    g.residual = A->residual;
+    g.y = A->y;
+    g.preact = A->preact;
+    g.group_list = A->group_list;
+    g.status = A->status;
+    g.m = A->m;
+    g.n = A->n;
+    g.k = A->k;
+    g.ld_res = A->ld_res;
+    g.ld_y = A->ld_y;
+    g.ld_z = A->ld_preact;
+    g.sfw_group_bytes = mxfp4_scales_row_bytes(A->n, A->k, 32, MXFP4_SCALES_MMA);
+    g.gl_type = A->group_list_type;
+    g.act = A->activation;
+    LnMaps maps;
+    memset(&maps, 0, sizeof(maps));
+    if (!encode_2d(&maps.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t*>(A->b), (uint64_t)kb,
+                   (uint64_t)(A->n * g.num_groups), (uint64_t)A->ldb, LN_ROW_BYTES, 128, CU_TENSOR_MAP_SWIZZLE_128B))
+        return MXFP4_ECUDA;
+    const bool f32 = A->d_dtype == MXFP4_F32;
+    return e2 ? launch_linear<MXFP4_ELEM_E2M1>(A, maps, g, kb, f32, s) : launch_linear<MXFP4_ELEM_E4M3>(A, maps, g, kb, f32, s);
+}
+
+static mxfp4_status run_linear_bwd(const mxfp4_linear_args* A, cudaStream_t s)
+{
+    mxfp4_status st = check_linear(A);
+    if (st != MXFP4_OK)
+        return st;
+    const bool gated = A->activation == MXFP4_ACT_SWIGLU;
+    const int64_t width = gated ? A->n / 2 : A->n;
+    const size_t esz = A->d_dtype == MXFP4_F32 ? 4 : 2;
+    const int64_t groups = A->group_list ? A->num_groups : 1;
+    if (A->ld_y < width || A->ld_preact < A->n || A->ld_grad < A->n)
+        return MXFP4_EINVAL;
+    if (A->n == 0)
+        return zero_status(A->status, s);
+    if (A->m > 0 && (!A->grad_out || !A->preact || !A->grad_preact))
+        return MXFP4_EINVAL;
+    if (!aligned(A->grad_out, esz) || !aligned(A->preact, esz) || !aligned(A->grad_preact, esz) || !aligned(A->grad_bias, 4) ||
+        !aligned(A->workspace, 4) || !aligned(A->status, 4))
+        return MXFP4_EINVAL;
+    if (A->grad_bias && (!A->workspace || A->workspace_bytes < mxfp4_grouped_linear_workspace(A->m, A->n, groups)))
+        return MXFP4_EINVAL;
+    LnBwdArgs b;
+    memset(&b, 0, sizeof(b));
+    b.grad = A->grad_out;
+    b.z = A->preact;
+    b.grad_z = A->grad_preact;
+    b.grad_bias = A->grad_bias;
+    b.ws = static_cast<float*>(A->workspace);
+    b.group_list = A->group_list;
+    b.status = A->status;
+    b.m = A->m;
+    b.n = A->n;
+    b.ld_g = A->ld_y;
+    b.ld_z = A->ld_preact;
+    b.ld_dz = A->ld_grad;
+    b.num_groups = (int32_t)groups;
+    b.gl_type = A->group_list_type;
+    b.act = A->activation;
+    const size_t plan = (size_t)(2 * (groups + 1)) * sizeof(int32_t);
+    const int per = (int)(16 / esz);
+    const bool vec = A->n % per == 0 && vec_rows(A->preact, A->ld_preact, esz) && vec_rows(A->grad_preact, A->ld_grad, esz) &&
+                     (gated ? aligned(A->grad_out, 8) && (A->ld_y * (int64_t)esz) % 8 == 0 : vec_rows(A->grad_out, A->ld_y, esz));
+    const void* fn = esz == 2 ? (vec ? (const void*)linear_bwd_kernel<2, true> : (const void*)linear_bwd_kernel<2, false>)
+                              : (vec ? (const void*)linear_bwd_kernel<4, true> : (const void*)linear_bwd_kernel<4, false>);
+    const int sms = device_sms(), occ = occupancy(fn, plan);
+    if (sms <= 0 || occ <= 0)
+        return MXFP4_ECUDA;
+    const int64_t ct = 32 * (vec ? per : 2);
+    const int64_t units = (A->m / LB_ROWS + groups) * ((A->n + ct - 1) / ct), most = (int64_t)sms * occ;
+    st = launch1(fn, units < most ? units : most, NTHREADS, plan, b, s);
+    if (st == MXFP4_OK && A->grad_bias) {
+        LnBwdArgs arg = b;
+        void* args[] = {&arg};
+        st = launched(cudaLaunchKernel((const void*)linear_bias_kernel, dim3((unsigned)((A->n + NTHREADS - 1) / NTHREADS), (unsigned)groups),
+                                       dim3(NTHREADS), args, plan, s));
+    }
+    return st;
+}
+
+}  // namespace mxfp4
+
+using namespace mxfp4;
+
+extern "C" {
+
+int64_t mxfp4_moe_route_workspace(int64_t tokens, int64_t experts)
+{
+    if (tokens < 0 || experts < 0)
+        return -1;
+    const int64_t chunks = route_chunks(tokens);
+    return chunks > 1 ? chunks * experts * (int64_t)sizeof(int32_t) : 0;
+}
+
+mxfp4_status mxfp4_moe_route(const mxfp4_moe_route_args* args, mxfp4_stream_t stream)
+{
+    return run_route(args, reinterpret_cast<cudaStream_t>(stream));
+}
+
+mxfp4_status mxfp4_moe_route_bwd(const mxfp4_moe_route_args* args, mxfp4_stream_t stream)
+{
+    return run_route_bwd(args, reinterpret_cast<cudaStream_t>(stream));
+}
+
+mxfp4_status mxfp4_moe_dispatch(const mxfp4_moe_move_args* args, mxfp4_stream_t stream)
+{
+    return run_dispatch(args, reinterpret_cast<cudaStream_t>(stream));
+}
+
+mxfp4_status mxfp4_moe_combine(const mxfp4_moe_move_args* args, mxfp4_stream_t stream)
+{
+    return run_combine(args, reinterpret_cast<cudaStream_t>(stream));
+}
+
+mxfp4_status mxfp4_moe_combine_bwd(const mxfp4_moe_move_args* args, mxfp4_stream_t stream)
+{
+    return run_combine_bwd(args, reinterpret_cast<cudaStream_t>(stream));
+}
+
+mxfp4_status mxfp4_grouped_linear(const mxfp4_linear_args* args, mxfp4_stream_t stream)
+{
+    return run_linear(args, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int64_t mxfp4_grouped_linear_workspace(int64_t m, int64_t n, int64_t num_groups)
+{
+    if (m < 0 || n < 0 || num_groups < 1)
+        return -1;
+    return (m / LB_ROWS + num_groups) * n * (int64_t)sizeof(float);
+}
+
+mxfp4_status mxfp4_grouped_linear_bwd(const mxfp4_linear_args* args, mxfp4_stream_t stream)
+{
+    return run_linear_bwd(args, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

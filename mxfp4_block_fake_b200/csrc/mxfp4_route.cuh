@@ -1,0 +1,446 @@
+// mxfp4_route.cuh -- routing of tokens to experts: selection, weights, the
+// expert-sorted order, and the gradient of the router's logits (included by
+// mxfp4_moe.cu; the definition is in include/mxfp4.h, mxfp4_moe_route).
+//
+// Selection is decided by real numbers (the keys s_e + b_e), so it must not
+// depend on how an exponential happens to round: keys are held in 64 bits.
+//
+// The order of the (token, expert) pairs by expert is a counting sort without
+// atomics on counters: a CTA takes RT_CHUNK consecutive tokens and keeps, per
+// expert, one bit per token that chose it (the only atomics set bits, whose
+// order cannot matter), so a pair's rank among its chunk's pairs of the same
+// expert is a population count. A scan of the chunks' counts per expert and
+// one of the experts' totals give every pair its row.
+
+namespace mxfp4 {
+
+constexpr int RT_THREADS = 256;
+constexpr int RT_WARPS = RT_THREADS / 32;
+constexpr int RT_CHUNK = 64;            // tokens per CTA: two words of token bits per expert
+constexpr int RT_MAX_EXPERTS = 1024;
+constexpr int RT_MAX_K = 32;            // a lane per chosen expert
+constexpr int RT_MAX_GROUPS = 32;       // a lane per group of experts
+
+struct RouteArgs {
+    const void* logits;
+    int64_t tokens, ld;
+    const float* bias;
+    const uint8_t* token_mask;
+    float* weights;
+    int32_t* experts_out;
+    int32_t* rows;
+    int32_t* slots;
+    int64_t* counts;
+    int32_t* ws;        // [chunks][experts]: counts of a chunk, then the rows before it
+    float scale;
+    int32_t experts, k, groups, topk_groups;
+    int32_t top2, sigmoid, renorm, bf16;
+    int32_t chunks;
+};
+
+__device__ __forceinline__ float rt_logit(const RouteArgs& a, int64_t t, int e)
+{
+    const int64_t i = t * a.ld + e;
+    return a.bf16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.logits)[i] << 16)
+                  : static_cast<const float*>(a.logits)[i];
+}
+
+__device__ __forceinline__ float warp_max(float v)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        v = fmaxf(v, __shfl_xor_sync(FULL, v, o));
+    return v;
+}
+
+template <typename T>
+__device__ __forceinline__ T warp_sum(T v)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+        v += __shfl_xor_sync(FULL, v, o);
+    return v;
+}
+
+__device__ __forceinline__ double rt_neg_inf() { return __longlong_as_double(0xFFF0000000000000ll); }
+
+// The chosen experts of token t in 64 bits: lane j < k returns the j-th (-1:
+// none). sk: the warp's scratch of a.experts doubles. m: the row's largest logit.
+__device__ __noinline__ int rt_select64(const RouteArgs& a, int64_t t, double* sk, float m)
+{
+    const int lane = threadIdx.x & 31, E = a.experts;
+    const double NI = rt_neg_inf();
+    double sum = 0.0;
+    __syncwarp();
+    for (int e = lane; e < E; e += 32) {
+        const double x = (double)rt_logit(a, t, e);
+        const double p = a.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - (double)m);
+        sk[e] = p;
+        sum += p;
+    }
+    sum = warp_sum(sum);
+    for (int e = lane; e < E; e += 32) {
+        double key = a.sigmoid ? sk[e] : sk[e] / sum;
+        bool open = rt_logit(a, t, e) > -INFINITY;
+        if (a.bias) {
+            const float b = a.bias[e];
+            key += (double)b;
+            open = open && fabsf(b) < INFINITY;
+        }
+        sk[e] = open ? key : NI;
+    }
+    __syncwarp();
+    if (a.groups > 1) {
+        // lane g: the rank of group g (best key, or the best two added)
+        const int per = E / a.groups;
+        double best = NI, next = NI;
+        if (lane < a.groups)
+            for (int i = 0; i < per; ++i) {
+                const double v = sk[lane * per + i];
+                if (v > best) {
+                    next = best;
+                    best = v;
+                } else if (v > next) {
+                    next = v;
+                }
+            }
+        const double rank = a.top2 && next != NI ? best + next : best;
+        int before = 0;
+        for (int g = 0; g < a.groups; ++g) {
+            const double r = __shfl_sync(FULL, rank, g);
+            before += r > rank || (r == rank && g < lane);
+        }
+        if (lane < a.groups && before >= a.topk_groups)
+            for (int i = 0; i < per; ++i)
+                sk[lane * per + i] = NI;
+        __syncwarp();
+    }
+    int mine = -1;
+    for (int j = 0; j < a.k; ++j) {
+        double best = NI;
+        int at = -1;
+        for (int e = lane; e < E; e += 32)
+            if (sk[e] > best) {
+                best = sk[e];
+                at = e;
+            }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+            const double v = __shfl_xor_sync(FULL, best, o);
+            const int w = __shfl_xor_sync(FULL, at, o);
+            if (w >= 0 && (at < 0 || v > best || (v == best && w < at))) {
+                best = v;
+                at = w;
+            }
+        }
+        if (at < 0)
+            break;  // no open expert is left (the same in every lane)
+        if (lane == (at & 31))
+            sk[at] = NI;
+        if (lane == j)
+            mine = at;
+        __syncwarp();
+    }
+    return mine;
+}
+
+// Score of a chosen expert (fp32): softmax e^(x - m) / sum, or the logistic
+// function. With renormalisation a common factor cancels, so scores that
+// underflow are taken relative to the chosen ones' largest logit.
+__device__ __forceinline__ float rt_sigmoid(float x)
+{
+    return x >= 0.0f ? 1.0f / (1.0f + expf(-x)) : expf(x) / (1.0f + expf(x));
+}
+
+__device__ __forceinline__ float rt_weight(const RouteArgs& a, int64_t t, int mine, float m, float sum)
+{
+    const float x = mine >= 0 ? rt_logit(a, t, mine) : -INFINITY;
+    float s;
+    if (a.renorm) {
+        const float top = warp_max(x);
+        if (a.sigmoid) {
+            const float shift = top < -60.0f ? top : 0.0f;  // below that 1 + e^x is 1
+            s = top < -60.0f ? expf(x - shift) : rt_sigmoid(x);
+        } else {
+            s = expf(x - top);
+        }
+        s = mine >= 0 ? s : 0.0f;
+        const float total = warp_sum(s);
+        return total > 0.0f ? a.scale * (s / total) : 0.0f;
+    }
+    s = a.sigmoid ? rt_sigmoid(x) : expf(x - m) / sum;
+    return mine >= 0 ? a.scale * s : 0.0f;
+}
+
+// Exclusive scan of n <= RT_MAX_EXPERTS counts (shared memory) into s_off by a
+// CTA of RT_THREADS; returns the total.
+__device__ int rt_scan(const int* s_cnt, int* s_off, int n)
+{
+    __shared__ int s_w[RT_WARPS];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (n + RT_THREADS - 1) / RT_THREADS;
+    int mine = 0;
+    for (int i = 0; i < per; ++i)
+        if (tid * per + i < n)
+            mine += s_cnt[tid * per + i];
+    int inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(FULL, inc, o);
+        inc += lane >= o ? v : 0;
+    }
+    if (lane == 31)
+        s_w[warp] = inc;
+    __syncthreads();
+    int off = inc - mine, total = 0;
+    for (int w = 0; w < RT_WARPS; ++w) {
+        off += w < warp ? s_w[w] : 0;
+        total += s_w[w];
+    }
+    for (int i = 0; i < per; ++i)
+        if (tid * per + i < n) {
+            s_off[tid * per + i] = off;
+            off += s_cnt[tid * per + i];
+        }
+    __syncthreads();
+    return total;
+}
+
+// One CTA per chunk. A single chunk (chunks == 1) finishes the order itself;
+// else `rows` receives ranks within the chunk and ws the chunk's counts.
+__global__ void __launch_bounds__(RT_THREADS) route_kernel(const RouteArgs a)
+{
+    extern __shared__ __align__(16) uint8_t rt_dyn[];
+    const int E = a.experts, K = a.k;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    double* s_key = reinterpret_cast<double*>(rt_dyn) + (size_t)warp * E;
+    uint32_t* s_bits = reinterpret_cast<uint32_t*>(rt_dyn + (size_t)RT_WARPS * E * 8);  // [E][2]
+    int16_t* s_pick = reinterpret_cast<int16_t*>(s_bits + 2 * E);                       // [RT_CHUNK][K]
+    const int64_t t0 = (int64_t)blockIdx.x * RT_CHUNK;
+    const int nt = (int)min((int64_t)RT_CHUNK, a.tokens - t0);
+    for (int i = tid; i < 2 * E; i += RT_THREADS)
+        s_bits[i] = 0u;
+    __syncthreads();
+    for (int i = warp; i < nt; i += RT_WARPS) {
+        const int64_t t = t0 + i;
+        int mine = -1;
+        float w = 0.0f;
+        if (!a.token_mask || a.token_mask[t]) {
+            float m = -INFINITY;
+            bool bad = false;
+            for (int e = lane; e < E; e += 32) {
+                const float x = rt_logit(a, t, e);
+                bad |= !(x < INFINITY);
+                m = fmaxf(m, x);
+            }
+            m = warp_max(m);
+            if (__any_sync(FULL, bad)) {
+                mine = lane < K ? lane : -1;
+                w = __uint_as_float(QNAN32);
+            } else if (m > -INFINITY) {
+                float sum = 0.0f;
+                if (!a.sigmoid && !a.renorm) {
+                    for (int e = lane; e < E; e += 32)
+                        sum += expf(rt_logit(a, t, e) - m);
+                    sum = warp_sum(sum);
+                }
+                mine = rt_select64(a, t, s_key, m);
+                w = rt_weight(a, t, mine, m, sum);
+            }
+        }
+        if (lane < K) {
+            a.weights[t * K + lane] = w;
+            a.experts_out[t * K + lane] = mine;
+            s_pick[i * K + lane] = (int16_t)mine;
+            if (mine >= 0)
+                atomicOr(&s_bits[2 * mine + (i >> 5)], 1u << (i & 31));
+        }
+    }
+    __syncthreads();
+    int* s_cnt = reinterpret_cast<int*>(rt_dyn);  // over the keys, which are done with
+    int* s_off = s_cnt + E;
+    if (a.chunks == 1) {
+        for (int e = tid; e < E; e += RT_THREADS) {
+            s_cnt[e] = __popc(s_bits[2 * e]) + __popc(s_bits[2 * e + 1]);
+            a.counts[e] = s_cnt[e];
+        }
+        __syncthreads();
+        const int total = rt_scan(s_cnt, s_off, E);
+        for (int p = total + tid; p < nt * K; p += RT_THREADS)
+            a.slots[p] = -1;
+    } else {
+        for (int e = tid; e < E; e += RT_THREADS)
+            a.ws[(int64_t)blockIdx.x * E + e] = __popc(s_bits[2 * e]) + __popc(s_bits[2 * e + 1]);
+    }
+    for (int p = tid; p < nt * K; p += RT_THREADS) {
+        const int e = s_pick[p], i = p / K;
+        int r = -1;
+        if (e >= 0) {
+            const uint32_t low = i < 32 ? s_bits[2 * e] : s_bits[2 * e + 1];
+            r = __popc(low & ((1u << (i & 31)) - 1u)) + (i < 32 ? 0 : __popc(s_bits[2 * e]));
+            if (a.chunks == 1) {
+                r += s_off[e];
+                a.slots[r] = p;
+            }
+        }
+        a.rows[t0 * K + p] = r;
+    }
+}
+
+// Exclusive scan of the chunks' counts per expert, in place, and the totals.
+// A CTA takes 32 experts; thread (lane, warp) a segment of the chunks.
+__global__ void __launch_bounds__(1024) route_scan_kernel(const RouteArgs a)
+{
+    __shared__ int s_seg[32][33];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int e = blockIdx.x * 32 + lane;
+    const int per = (a.chunks + 31) / 32;
+    const int c0 = min(a.chunks, warp * per), c1 = min(a.chunks, c0 + per);
+    int sum = 0;
+    if (e < a.experts)
+#pragma unroll 8
+        for (int c = c0; c < c1; ++c)
+            sum += a.ws[(int64_t)c * a.experts + e];
+    s_seg[warp][lane] = sum;
+    __syncthreads();
+    int off = 0, total = 0;
+    for (int w = 0; w < 32; ++w) {
+        const int v = s_seg[w][lane];
+        off += w < warp ? v : 0;
+        total += v;
+    }
+    if (e >= a.experts)
+        return;
+    if (warp == 0)
+        a.counts[e] = total;
+#pragma unroll 8
+    for (int c = c0; c < c1; ++c) {
+        const int64_t i = (int64_t)c * a.experts + e;
+        const int v = a.ws[i];
+        a.ws[i] = off;
+        off += v;
+    }
+}
+
+// Ranks within a chunk -> rows, and the rows' slots; -1 in the slots behind
+// the last row. One CTA per chunk.
+__global__ void __launch_bounds__(RT_THREADS) route_place_kernel(const RouteArgs a)
+{
+    __shared__ int s_cnt[RT_MAX_EXPERTS], s_off[RT_MAX_EXPERTS];
+    const int tid = threadIdx.x, E = a.experts, K = a.k;
+    for (int e = tid; e < E; e += RT_THREADS)
+        s_cnt[e] = (int)a.counts[e];
+    __syncthreads();
+    const int total = rt_scan(s_cnt, s_off, E);
+    const int64_t p0 = (int64_t)blockIdx.x * RT_CHUNK * K;
+    const int64_t pairs = a.tokens * K;
+    const int n = (int)min((int64_t)RT_CHUNK * K, pairs - p0);
+    for (int p = tid; p < n; p += RT_THREADS) {
+        const int e = a.experts_out[p0 + p];
+        if (e >= 0) {
+            const int r = a.rows[p0 + p] + a.ws[(int64_t)blockIdx.x * E + e] + s_off[e];
+            a.rows[p0 + p] = r;
+            a.slots[r] = (int)(p0 + p);
+        }
+        if (p0 + p >= total)
+            a.slots[p0 + p] = -1;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Gradient of the logits. With w_j = c s_j / S (S = the chosen scores' sum, or
+// 1), g_j the weights' gradients and h_j = c g_j / S:
+//   dL/ds_j = h_j - renorm * sum_i h_i s_i / S
+//   logistic: dL/dx_j = dL/ds_j s_j (1 - s_j) at the chosen experts, else 0
+//   softmax:  dL/dx_e = s_e (dL/ds_e - sum_j dL/ds_j s_j); renormalised, the
+//             sum is 0 and s_e / S is the softmax over the chosen logits
+// A warp per token. Rows with a NaN or +inf logit get NaN.
+// ---------------------------------------------------------------------------
+
+struct RouteBwdArgs {
+    RouteArgs r;              // logits, geometry, rule; experts_out is read
+    const float* grad_w;
+    void* grad_logits;
+    int64_t ld_g;
+};
+
+__device__ __forceinline__ void rt_store(const RouteBwdArgs& b, int64_t t, int e, float v)
+{
+    if (b.r.bf16)
+        static_cast<uint16_t*>(b.grad_logits)[t * b.ld_g + e] = (uint16_t)f32_to_bf16(v);
+    else
+        static_cast<float*>(b.grad_logits)[t * b.ld_g + e] = v;
+}
+
+__global__ void __launch_bounds__(RT_THREADS) route_bwd_kernel(const RouteBwdArgs b)
+{
+    extern __shared__ __align__(16) uint8_t rt_dyn[];
+    const RouteArgs& a = b.r;
+    const int E = a.experts, K = a.k;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    float* s_d = reinterpret_cast<float*>(rt_dyn) + (size_t)warp * E;  // dL/dx of the chosen experts
+    const int64_t t = (int64_t)blockIdx.x * RT_WARPS + warp;
+    if (t >= a.tokens)
+        return;
+    int mine = lane < K ? a.experts_out[t * K + lane] : -1;
+    mine = mine < E ? mine : -1;
+    const float g = mine >= 0 ? b.grad_w[t * K + lane] : 0.0f;
+    const bool some = __any_sync(FULL, mine >= 0);
+    float m = -INFINITY;
+    bool bad = false;
+    if (some)
+        for (int e = lane; e < E; e += 32) {
+            const float x = rt_logit(a, t, e);
+            bad |= !(x < INFINITY);
+            m = fmaxf(m, x);
+        }
+    bad = __any_sync(FULL, bad);
+    m = warp_max(m);
+    for (int e = lane; e < E; e += 32)
+        s_d[e] = bad ? __uint_as_float(QNAN32) : 0.0f;
+    __syncwarp();
+    float sub = 0.0f, sum = 1.0f;  // softmax as it is: what each s_e is multiplied by, and 1 / s_e's divisor
+    const bool dense = some && !bad && !a.sigmoid && !a.renorm;
+    if (some && !bad) {
+        const float x = mine >= 0 ? rt_logit(a, t, mine) : -INFINITY;
+        const float h = a.scale * g;
+        float d;
+        if (a.renorm) {
+            const float top = warp_max(x);
+            float s = a.sigmoid ? (top < -60.0f ? expf(x - top) : rt_sigmoid(x)) : expf(x - top);
+            s = mine >= 0 ? s : 0.0f;
+            const float total = warp_sum(s);
+            const float share = total > 0.0f ? s / total : 0.0f;
+            d = share * (h - warp_sum(h * share));
+            if (a.sigmoid)
+                d *= rt_sigmoid(-x);
+        } else if (a.sigmoid) {
+            d = h * rt_sigmoid(x) * rt_sigmoid(-x);
+        } else {
+            sum = 0.0f;
+            for (int e = lane; e < E; e += 32)
+                sum += expf(rt_logit(a, t, e) - m);
+            sum = warp_sum(sum);
+            d = h * expf(x - m) / sum;
+            sub = warp_sum(mine >= 0 ? d : 0.0f);
+        }
+        // an expert chosen twice takes the sum, in the slots' order
+        float total = 0.0f;
+        for (int j = 0; j < K; ++j) {
+            const int e = __shfl_sync(FULL, mine, j);
+            const float v = __shfl_sync(FULL, d, j);
+            total += e == mine ? v : 0.0f;
+        }
+        if (mine >= 0)
+            s_d[mine] = total;
+        __syncwarp();
+    }
+    for (int e = lane; e < E; e += 32) {
+        float v = s_d[e];
+        if (dense)
+            v -= expf(rt_logit(a, t, e) - m) / sum * sub;
+        rt_store(b, t, e, v);
+    }
+}
+
+}  // namespace mxfp4

@@ -45,7 +45,6 @@ constexpr int SG_TILE_BYTES = 4 * SG_SLAB_BYTES;           // 16384
 constexpr int SG_CODE_BYTES = SG_ROWS * SG_COLS / 2;       // 4096: e2m1 codes of a tile
 constexpr int SG_MASK_WORDS = SG_ROWS * SG_COLS / 32;      // 256: saturation bits of a tile
 constexpr int SG_STAGES = 3;
-constexpr uint64_t SG_WAIT_NS = 4000000000ull;             // an mbarrier wait gives up after 4 s
 
 // which outputs leave through TMA stores on full tiles (the others, and every
 // output of a group-tail or ragged tile, are copied out by the threads)
@@ -88,57 +87,6 @@ struct StagedMaps {
     CUtensorMap x, y, codes, mask, yr, codes_r, mask_r;
 };
 
-__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-
-
-__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count)
-{
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count));
-}
-
-__device__ __forceinline__ void mbar_expect_tx(uint32_t bar, uint32_t bytes)
-{
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-
-__device__ __forceinline__ void mbar_arrive(uint32_t bar)
-{
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-
-__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity)
-{
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return done != 0;
-}
-
-__device__ __forceinline__ uint64_t global_ns()
-{
-    uint64_t t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-
-// Wait for the phase of the given parity to complete; false after SG_WAIT_NS
-// of global time (the caller then records an error and stops).
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity)
-{
-    if (mbar_try(bar, parity))
-        return true;
-    const uint64_t t0 = global_ns();
-    while (!mbar_try(bar, parity))
-        if (global_ns() - t0 > SG_WAIT_NS)
-            return false;
-    return true;
-}
-
 // One 64 x 32 box of bf16 from global memory into a 4 KB swizzled slab. The
 // inner coordinate is a multiple of 64 elements (128 bytes).
 __device__ __forceinline__ void tma_load_slab(uint32_t dst, const CUtensorMap* map, int x, int y, uint32_t bar)
@@ -163,7 +111,6 @@ __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.comm
 __device__ __forceinline__ void bulk_wait_read_all() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_read_but1() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // A code-table entry. Not volatile: the table does not change once built, so
 // the compiler may schedule these loads freely among the surrounding work.
@@ -210,23 +157,6 @@ __device__ __forceinline__ uint32_t e2m1_word(const uint32_t* P)
     return r;
 }
 
-// Block exponent for a scale mode fixed at compile time (block_k's rule).
-template <int MODE>
-__device__ __forceinline__ int block_kt(uint32_t A, uint32_t thr)
-{
-    if constexpr (MODE == MXFP4_SCALE_FLOOR) {
-        return max((int)(A >> 23) - 129, -127);
-    } else {
-        const int k = (int)(A >> 23) - (int)(thr >> 23) + 1 - ((A & 0x7FFFFFu) < (thr & 0x7FFFFFu) ? 1 : 0);
-        return max(k, -30);
-    }
-}
-
-// Fast-path exponent range of this kernel: 2^k and every code * 2^k are
-// normal bf16 numbers (k >= -125), and the limit bits of lim16_of_k stay
-// below 0x8000 (k <= 16).
-__device__ __forceinline__ bool k_fast_bf(int k) { return (uint32_t)(k + 125) <= 141u; }
-
 // bf16 bits of 2^k for a fast-path k.
 __device__ __forceinline__ uint32_t bf16_pow2(int k) { return (uint32_t)(k + 127) << 7; }
 
@@ -263,32 +193,6 @@ __device__ __forceinline__ uint32_t qword(uint32_t wc, float inv_lo, float inv_h
     const uint32_t eh = lut_load((uint32_t)(t >> 32) * mul4 + lutb16);
     P = __byte_perm(el, eh, 0x7632) | (wc & 0x80008000u);
     return hmul2_bf16(P, s2);
-}
-
-// ---- E2M1 rounding by the hardware convert ---------------------------------
-// The convert rounds to nearest with ties to even; the codebook's rule sends
-// ties up (away from zero). Multiplying y by (1 + 2^-20) first moves exact
-// midpoints above themselves and nothing else across one: y is a bf16 value
-// times 2^-k (8 significant bits), so a y below a midpoint lies at least one
-// bf16 ulp (2^-8 relative) below it, and the one rounding of the product
-// changes it by at most 2^-24 relative. The product is formed as
-// x * (2^-k (1 + 2^-20)) + 0 in one fma: adding +0 turns -0 into +0 (the
-// codebook's sign rule for zero inputs) and keeps the sign of every nonzero
-// product, however small. Codes above 6 saturate to 6 in the convert, as in
-// the codebook. Checked against the table path for every finite bf16 value
-// and every fast-path k.
-
-// 2^-k (1 + 2^-20) for a fast-path k (mantissa bit 3 set).
-__device__ __forceinline__ float inv_nudged(int k) { return __uint_as_float((0x3F800000u - ((uint32_t)k << 23)) | 8u); }
-
-// 2^k for a fast-path k.
-__device__ __forceinline__ float pow2f_k(int k) { return __uint_as_float(0x3F800000u + ((uint32_t)k << 23)); }
-
-// Nudged scaled values of both halves of a bf16 word.
-__device__ __forceinline__ void nudged_pair(uint32_t w, float invn_lo, float invn_hi, float& ylo, float& yhi)
-{
-    asm("fma.rn.f32 %0, %1, %2, 0f00000000;" : "=f"(ylo) : "f"(__uint_as_float(w << 16)), "f"(invn_lo));
-    asm("fma.rn.f32 %0, %1, %2, 0f00000000;" : "=f"(yhi) : "f"(__uint_as_float(w & 0xFFFF0000u)), "f"(invn_hi));
 }
 
 // code * 2^k of both halves from the f16x2 codes, as packed bf16 (exact).
@@ -1348,20 +1252,6 @@ __global__ void __launch_bounds__(SB_THREADS, 1) qdq_staged128_kernel(const __gr
 // 32-byte aligned pointers and leading dimensions that are multiples of 16.
 // ---------------------------------------------------------------------------
 
-__device__ __forceinline__ void ld_nc_v8(const void* p, uint32_t* v)
-{
-    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-                 : "l"(p));
-}
-
-__device__ __forceinline__ void st_cs_v8(void* p, const uint32_t* v)
-{
-    asm volatile("st.global.cs.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]),
-                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
-}
-
 template <int MODE>
 __global__ void __launch_bounds__(NTHREADS) ste_row_kernel(const KArgs a)
 {
@@ -1423,25 +1313,6 @@ __global__ void __launch_bounds__(NTHREADS) ste_row_kernel(const KArgs a)
 // (SMMA: in the MMA layout). Without values this is the real-quantisation
 // producer. Blocks off the fast k range take the general element path.
 // ---------------------------------------------------------------------------
-
-// E2M1 bytes of four words sharing one scale, as one 32-bit nibble word.
-__device__ __forceinline__ uint32_t nibs4_cvt(const uint32_t* w, float invn)
-{
-    float y[8];
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-        nudged_pair(w[u], invn, invn, y[2 * u], y[2 * u + 1]);
-    uint32_t nibs;
-    asm("{\n\t.reg .b8 q0, q1, q2, q3;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 q0, %2, %1;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 q1, %4, %3;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 q2, %6, %5;\n\t"
-        "cvt.rn.satfinite.e2m1x2.f32 q3, %8, %7;\n\t"
-        "mov.b32 %0, {q0, q1, q2, q3};\n\t}"
-        : "=r"(nibs)
-        : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
-    return nibs;
-}
 
 template <int MODE, bool SMMA, bool VALS>
 __global__ void __launch_bounds__(NTHREADS) row_stream_kernel(const KArgs a)

@@ -583,3 +583,415 @@ def mxfp4_dual_level_qdq(x: torch.Tensor, *, level0_block: int = 512, scale_fact
     a.codes, a.scales0, a.scales1, a.mask = _ptr(r.codes), _ptr(r.scales0), _ptr(r.scales1), _ptr(r.mask)
     _abi.check(_abi.mxfp4_dual_level_qdq(a, _stream(dev)), "mxfp4_dual_level_qdq")
     return r
+
+
+# ---- mixture of experts ------------------------------------------------------
+
+_SCORES = {"softmax": _abi.SCORE_SOFTMAX, "sigmoid": _abi.SCORE_SIGMOID}
+_GROUP_SCORES = {"max": _abi.GROUP_BEST, "top2": _abi.GROUP_TOP2}
+_ACTIVATIONS = {"none": _abi.ACT_NONE, "relu": _abi.ACT_RELU, "gelu": _abi.ACT_GELU,
+                "gelu_tanh": _abi.ACT_GELU_TANH, "silu": _abi.ACT_SILU, "swiglu": _abi.ACT_SWIGLU}
+
+
+def _choose(table: dict, value, name: str) -> int:
+    if value not in table:
+        raise ValueError(f"{name} must be one of {tuple(table)}, got {value!r}")
+    return table[value]
+
+
+def _run(fn, args, device: torch.device, where: str) -> None:
+    """One library call on the current stream of the tensors' device."""
+    if device.index == torch.cuda.current_device():
+        st = fn(args, _stream(device))
+    else:
+        with torch.cuda.device(device):
+            st = fn(args, _stream(device))
+    if st:
+        _abi.check(st, where)
+
+
+def _on(t: torch.Tensor, name: str, device: torch.device, shape, dtype) -> torch.Tensor:
+    """An input of fixed shape and dtype on `device`, contiguous (copied if it is not)."""
+    if not isinstance(t, torch.Tensor) or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {list(t.shape)}, expected {list(shape)}")
+    return t if t.is_contiguous() else t.contiguous()
+
+
+def _rows2d(t: torch.Tensor, name: str, device: torch.device, dtype=None, shape=None) -> torch.Tensor:
+    """A 2-D fp32 / bf16 input with unit column stride and rows that do not
+    overlap (copied if it is not)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.device != device:
+        raise ValueError(f"{name} must be a CUDA tensor on {device}")
+    if t.ndim != 2:
+        raise ValueError(f"{name} must have two dimensions")
+    if t.dtype not in _DTYPES or (dtype is not None and t.dtype != dtype):
+        raise TypeError(f"{name} must be {dtype or 'float32 or bfloat16'}, got {t.dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {list(t.shape)}, expected {list(shape)}")
+    return t if rows_addressable(t.shape, t.stride()) else t.contiguous()
+
+
+def _out2d(t: torch.Tensor | None, name: str, shape, dtype, device) -> torch.Tensor:
+    """An output of this shape: a new tensor, or the caller's with unit column
+    stride and rows that do not overlap."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != dtype or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be a {dtype} CUDA tensor of shape {list(shape)} on {device}")
+    if not rows_addressable(t.shape, t.stride()):
+        raise ValueError(f"{name} must have unit column stride and non-overlapping rows")
+    return t
+
+
+def _cuda_device(t, name: str) -> torch.device:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (libmxfp4 has no CPU path)")
+    return t.device
+
+
+@dataclasses.dataclass
+class RouteResult:
+    weights: torch.Tensor  # fp32 [tokens, k]
+    experts: torch.Tensor  # int32 [tokens, k]; -1: none
+    rows: torch.Tensor     # int32 [tokens, k]: each pair's row of the expert-sorted order; -1: none
+    slots: torch.Tensor    # int32 [tokens * k]: each row's pair, token * k + slot; -1 behind the last row
+    counts: torch.Tensor   # int64 [experts]: rows per expert, a group_list of type 1
+
+
+def _route_args(logits: torch.Tensor, k: int, score: str, renormalize: bool, scale: float) -> _abi.RouteArgs:
+    a = _abi.RouteArgs()
+    a.logits = logits.data_ptr()
+    a.tokens, a.experts = logits.shape
+    a.ld = _ld(logits)
+    a.dtype = _DTYPES[logits.dtype]
+    a.k = k
+    a.score = _choose(_SCORES, score, "score")
+    a.renormalize = 1 if renormalize else 0
+    a.scale = float(scale)
+    return a
+
+
+def mxfp4_moe_route(logits: torch.Tensor, k: int, *, score: str = "softmax", bias: torch.Tensor | None = None,
+                    num_groups: int = 1, topk_groups: int | None = None, group_score: str = "top2",
+                    renormalize: bool = True, scale: float = 1.0,
+                    token_mask: torch.Tensor | None = None) -> RouteResult:
+    """Routing of tokens to experts (include/mxfp4.h, mxfp4_moe_route):
+    logits [tokens, experts] (float32 or bfloat16) -> the k experts of each
+    token, their weights, and the expert-sorted order of the (token, expert)
+    pairs. bias: float32 [experts], added to the scores for the choice only.
+    With num_groups > 1 only the topk_groups best groups of consecutive
+    experts stay open. token_mask: bool [tokens], False for padding. The
+    counts are a group_list (type 1) for the other entry points. Asynchronous."""
+    dev = _cuda_device(logits, "logits")
+    x = _rows2d(logits, "logits", dev)
+    t, e = x.shape
+    k = int(k)
+    a = _route_args(x, k, score, renormalize, scale)
+    a.num_groups = int(num_groups)
+    a.topk_groups = a.num_groups if topk_groups is None else int(topk_groups)
+    a.group_score = _choose(_GROUP_SCORES, group_score, "group_score")
+    if bias is not None:
+        bias = _on(bias, "bias", dev, (e,), torch.float32)
+        a.bias = bias.data_ptr()
+    if token_mask is not None:
+        token_mask = _on(token_mask, "token_mask", dev, (t,), torch.bool)
+        a.token_mask = token_mask.data_ptr()
+    if k < 1 or k > e:
+        raise ValueError(f"k must lie in [1, experts], got {k} of {e}")
+    i32 = dict(dtype=torch.int32, device=dev)
+    r = RouteResult(weights=torch.empty((t, k), dtype=torch.float32, device=dev), experts=torch.empty((t, k), **i32),
+                    rows=torch.empty((t, k), **i32), slots=torch.empty((t * k,), **i32),
+                    counts=torch.empty((e,), dtype=torch.int64, device=dev))
+    a.weights, a.chosen, a.rows = r.weights.data_ptr(), r.experts.data_ptr(), r.rows.data_ptr()
+    a.slots, a.counts = r.slots.data_ptr(), r.counts.data_ptr()
+    need = _abi.lib().mxfp4_moe_route_workspace(t, e)
+    if need > 0:
+        ws = torch.empty((need,), dtype=torch.uint8, device=dev)
+        a.workspace, a.workspace_bytes = ws.data_ptr(), need
+    _run(_abi.mxfp4_moe_route, a, dev, "mxfp4_moe_route")
+    return r
+
+
+def mxfp4_moe_route_bwd(grad_weights: torch.Tensor, logits: torch.Tensor, experts: torch.Tensor, *,
+                        score: str = "softmax", renormalize: bool = True, scale: float = 1.0,
+                        out: torch.Tensor | None = None) -> torch.Tensor:
+    """The logits' gradient of mxfp4_moe_route's weights, for the chosen
+    experts (int32 [tokens, k], the forward's). Asynchronous."""
+    dev = _cuda_device(logits, "logits")
+    x = _rows2d(logits, "logits", dev)
+    if not isinstance(experts, torch.Tensor) or experts.ndim != 2:
+        raise ValueError("experts must be an int32 CUDA tensor [tokens, k]")
+    t, k = x.shape[0], int(experts.shape[1])
+    experts = _on(experts, "experts", dev, (t, k), torch.int32)
+    grad_weights = _on(grad_weights, "grad_weights", dev, (t, k), torch.float32)
+    a = _route_args(x, k, score, renormalize, scale)
+    gx = _out2d(out, "out", x.shape, x.dtype, dev)
+    a.chosen, a.grad_weights, a.grad_logits, a.ld_grad = experts.data_ptr(), grad_weights.data_ptr(), gx.data_ptr(), _ld(gx)
+    _run(_abi.mxfp4_moe_route_bwd, a, dev, "mxfp4_moe_route_bwd")
+    return gx
+
+
+@dataclasses.dataclass
+class DispatchResult:
+    values: torch.Tensor | None = None
+    codes: torch.Tensor | None = None
+    scales: torch.Tensor | None = None  # E8M0, the MMA layout
+
+
+def _move_args(rows: torch.Tensor, dev: torch.device, tokens: int, cols: int, row_count: int, dtype):
+    if not isinstance(rows, torch.Tensor) or rows.ndim != 2:
+        raise ValueError("rows must be an int32 CUDA tensor [tokens, k]")
+    rows = _on(rows, "rows", dev, (tokens, rows.shape[1]), torch.int32)
+    a = _abi.MoveArgs()
+    a.rows = rows.data_ptr()
+    a.tokens, a.cols, a.row_count = tokens, cols, row_count
+    a.k = rows.shape[1]
+    a.dtype = _DTYPES[dtype]
+    return a, rows
+
+
+def mxfp4_moe_dispatch(x: torch.Tensor, rows: torch.Tensor, *, emit_values: bool = True, emit_codes: bool = False,
+                       elem_format: str = "e2m1", scale_mode: str = "page", scale_factor: float = 6.0,
+                       row_count: int | None = None, out: DispatchResult | None = None) -> DispatchResult:
+    """Token rows x [tokens, cols] copied to their experts' rows (rows int32
+    [tokens, k], of mxfp4_moe_route), as they are (values) and / or quantised
+    on the way to the operand of a block-scaled product (codes, and scales in
+    the MMA layout), as mxfp4_qdq_fwd quantises rows with block 32.
+    row_count defaults to tokens * k. Rows that no index names are left as
+    they were (undefined in new tensors). Asynchronous."""
+    dev = _cuda_device(x, "x")
+    x = _rows2d(x, "x", dev)
+    t, cols = x.shape
+    n = int(rows.numel() if row_count is None else row_count)
+    a, rows = _move_args(rows, dev, t, cols, n, x.dtype)
+    a.x, a.ld_tokens = x.data_ptr(), _ld(x)
+    fmt = _elem_format(elem_format)
+    width = cols if fmt == _abi.ELEM_E4M3 else (cols + 1) // 2
+    u8 = dict(dtype=torch.uint8, device=dev)
+    nbytes = scales_row_bytes(n, cols, 32, "mma") if emit_codes or (out is not None and out.codes is not None) else 0
+    if out is None:
+        if not emit_values and not emit_codes:
+            raise ValueError("at least one of emit_values / emit_codes must be set")
+        r = DispatchResult()
+        if emit_values:
+            r.values = torch.empty((n, cols), dtype=x.dtype, device=dev)
+        if emit_codes:
+            r.codes, r.scales = torch.empty((n, width), **u8), torch.empty((nbytes,), **u8)
+    else:
+        r = out
+        if r.values is None and r.codes is None:
+            raise ValueError("out holds neither values nor codes")
+        if r.values is not None:
+            _out2d(r.values, "values", (n, cols), x.dtype, dev)
+        if r.codes is not None:
+            _need(r.codes, "codes", (n, width), torch.uint8, dev)
+            if r.scales is None:
+                raise ValueError("codes need scales")
+            _need(r.scales, "scales", (nbytes,), torch.uint8, dev, min_rows=nbytes)
+    if r.values is not None:
+        a.values, a.ld_rows = r.values.data_ptr(), _ld(r.values)
+    if r.codes is not None:
+        a.codes, a.scales = r.codes.data_ptr(), r.scales.data_ptr()
+        a.elem_format, a.scale_mode = fmt, _choose(_MODES, scale_mode, "scale_mode")
+        a.scale_factor = float(scale_factor)
+    _run(_abi.mxfp4_moe_dispatch, a, dev, "mxfp4_moe_dispatch")
+    return r
+
+
+def mxfp4_moe_combine(y: torch.Tensor, rows: torch.Tensor, weights: torch.Tensor | None = None, *,
+                      residual: torch.Tensor | None = None, out: torch.Tensor | None = None) -> torch.Tensor:
+    """out[t] = residual[t] + sum_j weights[t, j] y[rows[t, j]] over the expert
+    rows y [row_count, cols] (weights None: ones; skipped indices add nothing);
+    summed in fp32, in y's dtype. out may be residual. Asynchronous."""
+    dev = _cuda_device(y, "y")
+    y = _rows2d(y, "y", dev)
+    n, cols = y.shape
+    t = int(rows.shape[0]) if isinstance(rows, torch.Tensor) and rows.ndim == 2 else 0
+    a, rows = _move_args(rows, dev, t, cols, n, y.dtype)
+    a.y, a.ld_rows = y.data_ptr(), _ld(y)
+    if weights is not None:
+        weights = _on(weights, "weights", dev, rows.shape, torch.float32)
+        a.weights = weights.data_ptr()
+    if residual is not None:
+        residual = _rows2d(residual, "residual", dev, y.dtype, (t, cols))
+        a.residual, a.ld_tokens = residual.data_ptr(), _ld(residual)
+    o = _out2d(out, "out", (t, cols), y.dtype, dev)
+    a.out, a.ld_out = o.data_ptr(), _ld(o)
+    _run(_abi.mxfp4_moe_combine, a, dev, "mxfp4_moe_combine")
+    return o
+
+
+def mxfp4_moe_combine_bwd(grad_out: torch.Tensor, y: torch.Tensor | None, rows: torch.Tensor,
+                          weights: torch.Tensor | None = None, *, grad_rows: bool = True, grad_weights: bool = True,
+                          row_count: int | None = None, out: torch.Tensor | None = None):
+    """Gradients of mxfp4_moe_combine: (grad of y's rows, grad of the
+    weights), each None unless asked for. y is read for the weights' gradient
+    only. Rows that no index names are left as they were (out, or undefined in
+    a new tensor). Asynchronous."""
+    dev = _cuda_device(grad_out, "grad_out")
+    g = _rows2d(grad_out, "grad_out", dev)
+    t, cols = g.shape
+    if not grad_rows and not grad_weights:
+        raise ValueError("at least one of grad_rows / grad_weights must be set")
+    if grad_weights and y is None:
+        raise ValueError("the weights' gradient needs y")
+    if y is not None:
+        y = _rows2d(y, "y", dev, g.dtype)
+        if y.shape[1] != cols:
+            raise ValueError(f"y has {y.shape[1]} columns, expected {cols}")
+    n = int(row_count) if row_count is not None else int(rows.numel() if y is None else y.shape[0])
+    if y is not None and y.shape[0] != n:
+        raise ValueError(f"y has {y.shape[0]} rows, expected {n}")
+    a, rows = _move_args(rows, dev, t, cols, n, g.dtype)
+    a.grad_out, a.ld_out = g.data_ptr(), _ld(g)
+    if weights is not None:
+        weights = _on(weights, "weights", dev, rows.shape, torch.float32)
+        a.weights = weights.data_ptr()
+    gy = gw = None
+    if grad_weights:
+        a.y, a.ld_rows = y.data_ptr(), _ld(y)
+        gw = torch.empty(rows.shape, dtype=torch.float32, device=dev)
+        a.grad_weights = gw.data_ptr()
+    if grad_rows:
+        gy = _out2d(out, "out", (n, cols), g.dtype, dev)
+        a.grad_rows, a.ld_grad_rows = gy.data_ptr(), _ld(gy)
+    _run(_abi.mxfp4_moe_combine_bwd, a, dev, "mxfp4_moe_combine_bwd")
+    return gy, gw
+
+
+@dataclasses.dataclass
+class LinearResult:
+    y: torch.Tensor
+    preact: torch.Tensor | None = None
+    status: torch.Tensor | None = None
+
+
+_CODE_DTYPES = (torch.uint8, torch.float4_e2m1fn_x2, torch.float8_e4m3fn, torch.float8_e8m0fnu)
+
+
+def _code_bytes(t: torch.Tensor, name: str, device: torch.device) -> torch.Tensor:
+    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype not in _CODE_DTYPES:
+        raise ValueError(f"{name} must be a uint8 (or fp4 / fp8 / e8m0) CUDA tensor on {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t if t.dtype == torch.uint8 else t.view(torch.uint8)
+
+
+def _linear_groups(a: _abi.LinearArgs, group_list, group_list_type: int, dev: torch.device):
+    if group_list is None:
+        return None, 1
+    gl, ng = _group_args(group_list, group_list_type, dev)
+    if gl.device != dev:
+        raise ValueError(f"group_list must be a CUDA tensor on {dev}")
+    a.group_list, a.num_groups, a.group_list_type = gl.data_ptr(), ng, int(group_list_type)
+    return gl, ng
+
+
+def mxfp4_grouped_linear(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tensor, b_scales: torch.Tensor,
+                         group_list=None, *, k: int, elem_format: str = "e2m1", group_list_type: int = 0,
+                         bias: torch.Tensor | None = None, activation: str = "none",
+                         residual: torch.Tensor | None = None, out_dtype=torch.bfloat16, emit_preact: bool = False,
+                         check: bool | None = None, out: LinearResult | None = None) -> LinearResult:
+    """act(A B_g^T + bias_g) + residual on block-scaled operands (include/
+    mxfp4.h, mxfp4_grouped_linear), one kernel. a: [m, row bytes] codes and
+    a_scales their MMA-layout scales; b: [G, n, row bytes] (or [G * n, row
+    bytes]) and b_scales G consecutive scale buffers; group_list splits the
+    rows of a (None: one group). bias: float32 [G, n] (or [n] for one group).
+    activation: none, relu, gelu, gelu_tanh, silu, or swiglu (columns 2j and
+    2j + 1 are gate and up; y has n / 2 columns). emit_preact also returns the
+    pre-activation for mxfp4_grouped_linear_bwd. The groups may end before
+    row m; rows behind them are left as they were (undefined in new tensors).
+    check (the default with a group_list) synchronises and raises for an
+    invalid list; with check=False read the returned status."""
+    dev = _cuda_device(a, "a")
+    fmt = _elem_format(elem_format)
+    act = _choose(_ACTIVATIONS, activation, "activation")
+    k = int(k)
+    kb = k // 2 if fmt == _abi.ELEM_E2M1 else k
+    if k <= 0 or k % (64 if fmt == _abi.ELEM_E2M1 else 32):
+        raise ValueError("k must be a positive multiple of 64 (e2m1) or 32 (e4m3)")
+    a8, b8 = _code_bytes(a, "a", dev), _code_bytes(b, "b", dev)
+    as8, bs8 = _code_bytes(a_scales, "a_scales", dev), _code_bytes(b_scales, "b_scales", dev)
+    if a8.ndim != 2 or b8.ndim not in (2, 3):
+        raise ValueError("a must be [m, row bytes], b [G, n, row bytes] or [G * n, row bytes]")
+    if a8.shape[1] < kb or b8.shape[-1] < kb:
+        raise ValueError("operand rows are shorter than k")
+    if out_dtype not in _DTYPES:
+        raise ValueError("out_dtype must be float32 or bfloat16")
+    g = _abi.LinearArgs()
+    gl, ng = _linear_groups(g, group_list, group_list_type, dev)
+    m, b_rows = a8.shape[0], b8.numel() // b8.shape[-1] if b8.shape[-1] else 0
+    if b_rows % ng or (b8.ndim == 3 and b8.shape[0] != ng):
+        raise ValueError("b must stack one matrix of n rows per group")
+    n = b_rows // ng
+    if act == _abi.ACT_SWIGLU and n % 2:
+        raise ValueError("swiglu needs an even number of columns (gate and up alternate)")
+    width = n // 2 if act == _abi.ACT_SWIGLU else n
+    if as8.numel() < scales_row_bytes(m, k, 32, "mma"):
+        raise ValueError("a_scales is smaller than mxfp4_scales_row_bytes()")
+    if bs8.numel() < ng * scales_row_bytes(n, k, 32, "mma"):
+        raise ValueError("b_scales is smaller than one mxfp4_scales_row_bytes() per group")
+    g.elem_format, g.activation = fmt, act
+    g.m, g.n, g.k = m, n, k
+    g.a, g.lda, g.a_scales = a8.data_ptr(), a8.shape[1], as8.data_ptr()
+    g.b, g.ldb, g.b_scales = b8.data_ptr(), b8.shape[-1], bs8.data_ptr()
+    g.d_dtype = _DTYPES[out_dtype]
+    if bias is not None:
+        bias = _on(bias, "bias", dev, (n,) if bias.ndim == 1 and ng == 1 else (ng, n), torch.float32)
+        g.bias = bias.data_ptr()
+    if residual is not None:
+        residual = _rows2d(residual, "residual", dev, out_dtype, (m, width))
+        g.residual, g.ld_res = residual.data_ptr(), _ld(residual)
+    r = LinearResult(y=_out2d(None if out is None else out.y, "y", (m, width), out_dtype, dev))
+    g.y, g.ld_y = r.y.data_ptr(), _ld(r.y)
+    if emit_preact or (out is not None and out.preact is not None):
+        r.preact = _out2d(None if out is None else out.preact, "preact", (m, n), out_dtype, dev)
+        g.preact, g.ld_preact = r.preact.data_ptr(), _ld(r.preact)
+    if gl is not None:
+        r.status = torch.empty((1,), dtype=torch.int32, device=dev)
+        g.status = r.status.data_ptr()
+    _run(_abi.mxfp4_grouped_linear, g, dev, "mxfp4_grouped_linear")
+    if gl is not None and (check is None or check):
+        _check_status(r.status, "mxfp4_grouped_linear")
+    return r
+
+
+def mxfp4_grouped_linear_bwd(grad_out: torch.Tensor, preact: torch.Tensor, group_list=None, *,
+                             group_list_type: int = 0, activation: str = "none", bias_grad: bool = True,
+                             check: bool | None = None, out: torch.Tensor | None = None):
+    """Gradients of mxfp4_grouped_linear's epilogue: (grad of the
+    pre-activation [m, n] in preact's dtype, grad of the bias float32 [G, n]
+    or None). The products of the operands' gradients take the former
+    (mxfp4_qdq_fwd, mxfp4_grouped_gemm). Rows behind the groups are left as
+    they were (undefined in a new tensor). check as in mxfp4_grouped_linear."""
+    dev = _cuda_device(preact, "preact")
+    z = _rows2d(preact, "preact", dev)
+    m, n = z.shape
+    act = _choose(_ACTIVATIONS, activation, "activation")
+    if act == _abi.ACT_SWIGLU and n % 2:
+        raise ValueError("swiglu needs an even number of columns (gate and up alternate)")
+    gy = _rows2d(grad_out, "grad_out", dev, z.dtype, (m, n // 2 if act == _abi.ACT_SWIGLU else n))
+    g = _abi.LinearArgs()
+    gl, ng = _linear_groups(g, group_list, group_list_type, dev)
+    g.activation, g.m, g.n, g.d_dtype = act, m, n, _DTYPES[z.dtype]
+    g.grad_out, g.ld_y = gy.data_ptr(), _ld(gy)
+    g.preact, g.ld_preact = z.data_ptr(), _ld(z)
+    gz = _out2d(out, "out", (m, n), z.dtype, dev)
+    g.grad_preact, g.ld_grad = gz.data_ptr(), _ld(gz)
+    gb = status = None
+    if bias_grad:
+        gb = torch.empty((ng, n), dtype=torch.float32, device=dev)
+        need = _abi.lib().mxfp4_grouped_linear_workspace(m, n, ng)
+        ws = torch.empty((need,), dtype=torch.uint8, device=dev)
+        g.grad_bias, g.workspace, g.workspace_bytes = gb.data_ptr(), ws.data_ptr(), need
+    if gl is not None:
+        status = torch.empty((1,), dtype=torch.int32, device=dev)
+        g.status = status.data_ptr()
+    _run(_abi.mxfp4_grouped_linear_bwd, g, dev, "mxfp4_grouped_linear_bwd")
+    if gl is not None and (check is None or check):
+        _check_status(status, "mxfp4_grouped_linear_bwd")
+    return gz, gb

@@ -1,0 +1,756 @@
+"""GPU checks of the mixture-of-experts operators against their definitions in
+64 bits (tests/moe_ref.py) and against the oracle's quantiser.
+
+Tolerances count roundings of half a step: fp32 2^-24, bf16 2^-8 relative to
+the value. The bounds are written beside each check.
+"""
+from __future__ import annotations
+
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from mxfp4_block_fake_b200 import MXFP4ArgumentError, ops
+from tests import moe_ref as R
+
+pytestmark = pytest.mark.gpu
+
+U32, U16 = 2.0 ** -24, 2.0 ** -8
+DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def rnd(*shape, seed=0, std=1.0, dtype=torch.float32):
+    return (torch.randn(*shape, generator=gen(seed)) * std).to(dtype)
+
+
+def close(got, want, bound, what=""):
+    got, want = got.detach().double().cpu(), want.double()
+    bound = torch.as_tensor(bound, dtype=torch.float64).expand_as(want)
+    assert got.shape == want.shape, what
+    assert torch.equal(torch.isnan(got), torch.isnan(want)), what
+    err = torch.where(torch.isnan(want), 0.0, (got - want).abs())
+    worst = (err / (bound + 1e-300)).max() if err.numel() else torch.tensor(0.0)
+    assert bool((err <= bound + 1e-300).all()), f"{what}: error / bound {float(worst):.3g}"
+
+
+# ---------------------------------------------------------------------------- routing
+
+def check_route(x, k, token_mask=None, bias=None, **kw):
+    """x: CPU logits. Experts and the order exactly, weights within the fp32
+    evaluation: a score is an exponential of x - m (or x), whose rounding
+    moves it by |x - m| 2^-24 relative, at most 2 ulp of expf, a sum of at
+    most E terms in a tree of E/32 + 5 additions, and three more operations."""
+    dev = "cuda"
+    r = ops.mxfp4_moe_route(x.to(dev), k, token_mask=None if token_mask is None else token_mask.to(dev),
+                            bias=None if bias is None else bias.to(dev), **kw)
+    weights, experts = R.route(x, k, token_mask=token_mask, bias=bias, **kw)
+    e = x.shape[1]
+    rows, slots, counts = R.plan(experts, e)
+    t = x.shape[0]
+    assert r.experts.cpu().tolist() == experts
+    assert r.rows.cpu().tolist() == rows and r.slots.cpu().tolist() == slots and r.counts.cpu().tolist() == counts
+    w = torch.tensor(weights, dtype=torch.float64).view(t, k)
+    spread = x.double().nan_to_num(0.0, 0.0, 0.0).abs().max().item() * 2 if x.numel() else 0.0
+    close(r.weights, w, (spread + 2 * 4 + e / 32 + 5 + 8) * U32 * w.nan_to_num(0.0).abs(), "weights")
+    return r
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalize", [True, False])
+@pytest.mark.parametrize("tokens,experts,k", [(1, 1, 1), (1, 256, 8), (3, 7, 7), (64, 60, 4), (65, 33, 2), (200, 1024, 32), (333, 64, 6)])
+def test_route(dtype, score, renormalize, tokens, experts, k):
+    x = rnd(tokens, experts, seed=tokens, std=1.5, dtype=DT[dtype])
+    check_route(x, k, score=score, renormalize=renormalize, scale=2.5)
+
+
+@pytest.mark.parametrize("group_score", ["top2", "max"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("experts,groups,topk_groups,k", [(256, 8, 4, 8), (60, 4, 2, 5), (32, 32, 3, 3), (96, 3, 1, 7), (264, 8, 8, 8),
+                                                          (1024, 2, 1, 4), (160, 5, 3, 6)])
+@pytest.mark.parametrize("with_bias", [True, False])
+def test_route_groups(group_score, score, experts, groups, topk_groups, k, with_bias):
+    x = rnd(130, experts, seed=experts, std=1.5)
+    bias = rnd(experts, seed=5, std=0.05) if with_bias else None
+    check_route(x, k, score=score, bias=bias, num_groups=groups, topk_groups=topk_groups, group_score=group_score)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups", [1, 4])
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_route_special_rows(score, groups, with_bias):
+    """Ties, closed experts, rows without any, NaN and +inf, masked rows that hold them."""
+    e, k = 40, 6
+    x = rnd(100, e, seed=3, dtype=torch.bfloat16).float()
+    x[0] = 0.0                       # all equal: the lowest experts
+    x[1] = -torch.inf                # nothing is open
+    x[2, :37] = -torch.inf           # three open experts
+    x[3, 11] = torch.nan
+    x[4, 39] = torch.inf
+    x[5] = -120.0                    # scores that underflow in fp32 next to 1
+    x[5, 7] = -119.0
+    x[6, ::2] = x[6, 1::2]           # pairs of equals
+    x[7] = 3.0e38
+    x[8] = -3.0e38 if score == "softmax" else -80.0
+    x[9] = torch.nan
+    x[10, 1:] = -torch.inf
+    x[11] = 1.0e-42                  # subnormals
+    mask = torch.ones(100, dtype=torch.bool)
+    mask[9] = mask[20:25] = mask[99] = False
+    bias = None
+    if with_bias:
+        bias = rnd(e, seed=4, std=0.02)
+        bias[3], bias[5], bias[30] = torch.nan, torch.inf, -torch.inf
+    for renormalize in (True, False):
+        check_route(x, k, token_mask=mask, score=score, bias=bias, num_groups=groups, topk_groups=max(1, groups // 2),
+                    renormalize=renormalize)
+
+
+def test_route_near_ties_are_decided_in_64_bits():
+    """Keys s + b that fp32 cannot tell apart: b is set so that neighbours' keys
+    differ by 1e-9 (fp32 steps near 0.5 are 6e-8)."""
+    e, k = 64, 8
+    x = rnd(256, e, seed=9, std=0.5)
+    # the same logits in every token, in a different order of the experts
+    base = x[0].double()
+    s = torch.sigmoid(base)
+    order = torch.randperm(e, generator=gen(1))
+    want = torch.empty(e, dtype=torch.float64)
+    want[order] = 0.6 + 1e-9 * torch.arange(e, dtype=torch.float64)
+    bias = (want - s).float()        # fp32: the keys now differ by its rounding, about 1e-9 to 1e-8
+    x[:] = x[0]
+    x[1::2] += rnd(128, e, seed=10, std=1e-7)
+    check_route(x, k, score="sigmoid", bias=bias)
+    check_route(x, k, score="sigmoid", bias=bias, num_groups=8, topk_groups=3)
+    check_route(x, k, score="softmax", bias=(0.6 - torch.softmax(base, 0) + 1e-9 * order.double()).float(), num_groups=4, topk_groups=2)
+
+
+@pytest.mark.parametrize("tokens", [0, 1, 64, 65, 2048, 2049, 5000])
+def test_route_order_of_many_tokens(tokens):
+    """The expert-sorted order against a stable sort (experts from the call)."""
+    e, k = 48, 4
+    x = rnd(tokens, e, seed=2, std=2.0).cuda()
+    mask = (torch.rand(tokens, generator=gen(7)) > 0.3).cuda()
+    r = ops.mxfp4_moe_route(x, k, token_mask=mask)
+    flat = r.experts.reshape(-1).long()
+    total = int((flat >= 0).sum())
+    key = torch.where(flat < 0, e, flat)
+    order = torch.sort(key, stable=True).indices[:total]
+    assert torch.equal(r.slots[:total].long(), order) and bool((r.slots[total:] == -1).all())
+    rows = torch.full_like(flat, -1)
+    rows[order] = torch.arange(total, device="cuda")
+    assert torch.equal(r.rows.reshape(-1).long(), rows)
+    assert torch.equal(r.counts, torch.bincount(key, minlength=e + 1)[:e])
+    assert torch.equal(torch.sort(r.experts[mask], 1).values, torch.sort(torch.topk(x[mask], k, 1).indices.int(), 1).values)
+
+
+def test_route_strided_logits_and_repeatability():
+    big = rnd(130, 90, seed=8, dtype=torch.bfloat16).cuda()
+    x = big[:, 3:63]
+    a = ops.mxfp4_moe_route(x, 5)
+    b = ops.mxfp4_moe_route(x.contiguous(), 5)
+    c = ops.mxfp4_moe_route(big.t().contiguous().t()[:, 3:63], 5)
+    for f in ("weights", "experts", "rows", "slots", "counts"):
+        assert torch.equal(getattr(a, f), getattr(b, f)) and torch.equal(getattr(a, f), getattr(c, f))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalize", [True, False])
+@pytest.mark.parametrize("tokens,experts,k", [(1, 1, 1), (5, 7, 7), (70, 256, 8), (33, 1000, 32)])
+def test_route_backward(dtype, score, renormalize, tokens, experts, k):
+    """Against autograd of the formula in 64 bits. With c = scale and G = max
+    |g| a gradient is a sum of at most k + 1 products of scores (<= 1) and c g;
+    every factor carries the weights' relative error."""
+    x = rnd(tokens, experts, seed=11, std=1.5, dtype=DT[dtype])
+    g = rnd(tokens, k, seed=12)
+    chosen = torch.topk(x.double(), k, 1).indices.int()
+    if tokens > 4:
+        chosen[1] = -1                 # a token without experts
+        chosen[2, k // 2:] = -1        # a token with fewer
+    scale = 1.5
+    got = ops.mxfp4_moe_route_bwd(g.cuda(), x.cuda(), chosen.cuda(), score=score, renormalize=renormalize, scale=scale)
+    v = x.double().requires_grad_(True)
+    w = R.route_weights(v, chosen, score, renormalize, scale)
+    (want,) = torch.autograd.grad(w, v, g.double())
+    top = scale * g.abs().double().amax(1, keepdim=True) * (2 if renormalize else 1)
+    unit = (2 * 2 * x.double().abs().max().item() + 2 * 8 + 2 * (experts / 32 + 5) + k + 12) * U32
+    # every gradient entry is at most top; its terms' errors are unit * top each
+    close(got, want, 2 * unit * top + (U16 * want.abs() if dtype == "bf16" else U32 * want.abs()), "grad_logits")
+
+
+def test_route_backward_against_differences():
+    x = rnd(6, 20, seed=13)
+    chosen = torch.topk(x, 3, 1).indices.int()
+    g = rnd(6, 3, seed=14)
+    for score in ("softmax", "sigmoid"):
+        for renormalize in (True, False):
+            got = ops.mxfp4_moe_route_bwd(g.cuda(), x.cuda(), chosen.cuda(), score=score, renormalize=renormalize).cpu().double()
+            h = 1e-5
+            for e in range(20):
+                d = torch.zeros(20, dtype=torch.float64)
+                d[e] = h
+                up = (R.route_weights(x.double() + d, chosen, score, renormalize, 1.0) * g).sum(1)
+                down = (R.route_weights(x.double() - d, chosen, score, renormalize, 1.0) * g).sum(1)
+                # central differences: h^2 times a third derivative below 10 max|g|, and 1e-16 / h of rounding
+                assert ((up - down) / (2 * h) - got[:, e]).abs().max() < 1e-5
+
+
+def test_route_backward_special_rows():
+    x = rnd(6, 16, seed=15)
+    x[0, 3] = torch.nan
+    x[1, 4] = torch.inf
+    x[2, 5:] = -torch.inf
+    x[3] = torch.nan
+    chosen = torch.topk(x.nan_to_num(0.0), 2, 1).indices.int()
+    chosen[3] = -1
+    chosen[4] = 7                        # the same expert twice: the sum of both
+    g = rnd(6, 2, seed=16)
+    for score in ("softmax", "sigmoid"):
+        got = ops.mxfp4_moe_route_bwd(g.cuda(), x.cuda(), chosen.cuda(), score=score, renormalize=False).cpu()
+        assert bool(torch.isnan(got[0]).all()) and bool(torch.isnan(got[1]).all()) and bool((got[3] == 0).all())
+        assert bool((got[2, 5:] == 0).all()) and bool(torch.isfinite(got[2]).all())
+        v = x[4:5].double().requires_grad_(True)
+        (want,) = torch.autograd.grad(R.route_weights(v, chosen[4:5], score, False, 1.0), v, g[4:5].double())
+        close(got[4:5], want, 64 * U32 * g[4].abs().sum().double(), "twice")
+    wild = chosen.clone()
+    wild[5] = 99                         # outside the experts: ignored
+    got = ops.mxfp4_moe_route_bwd(g.cuda(), x.cuda(), wild.cuda(), renormalize=True).cpu()
+    assert bool((got[5] == 0).all())
+
+
+# ------------------------------------------------------------------ dispatch and combine
+
+def a_plan(tokens, experts, k, seed=0, masked=0.0):
+    g = gen(seed)
+    chosen = torch.stack([torch.randperm(experts, generator=g)[:k] for _ in range(tokens)]).int() if tokens else torch.zeros(0, k, dtype=torch.int32)
+    if masked and tokens:
+        chosen[torch.rand(tokens, generator=g) < masked] = -1
+        chosen[torch.rand(tokens, generator=g) < masked, -1] = -1
+    rows, slots, counts = R.plan(chosen.tolist(), experts)
+    return (torch.tensor(rows, dtype=torch.int32).view(tokens, k), torch.tensor(slots, dtype=torch.int32),
+            torch.tensor(counts, dtype=torch.int64))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("tokens,k,cols", [(1, 1, 1), (5, 3, 64), (130, 8, 96), (67, 2, 1001), (33, 4, 7168)])
+def test_dispatch_values(dtype, tokens, k, cols):
+    rows, slots, _ = a_plan(tokens, 12, k, masked=0.2)
+    x = rnd(tokens, cols, seed=1, dtype=DT[dtype])
+    out = torch.full((tokens * k + 3, cols), 7.0, dtype=DT[dtype], device="cuda")
+    r = ops.mxfp4_moe_dispatch(x.cuda(), rows.cuda(), row_count=tokens * k + 3, out=ops.DispatchResult(values=out))
+    want = torch.full_like(out, 7.0).cpu()          # rows that no index names stay
+    total = int((slots >= 0).sum())
+    want[:total] = x[slots[:total].long() // k]
+    assert torch.equal(r.values.cpu(), want)
+
+
+@pytest.mark.parametrize("fmt,mode", [("e2m1", "page"), ("e2m1", "floor"), ("e4m3", "floor")])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("tokens,k,cols", [(1, 1, 32), (3, 8, 128), (70, 3, 4128), (40, 2, 77), (9, 1, 7168), (50, 5, 192), (20, 3, 33)])
+def test_dispatch_quantised(fmt, mode, dtype, tokens, k, cols):
+    """Byte for byte the oracle's row-wise quantisation of the token's row, in
+    the rows the plan names; other rows and their scales stay."""
+    rows, slots, _ = a_plan(tokens, 10, k, seed=3, masked=0.2 if tokens > 5 else 0.0)
+    x = rnd(tokens, cols, seed=2, std=3.0)
+    x[:, ::17] *= 1000.0
+    if cols > 60:
+        x[0, :32] = 0.0
+        x[-1, 32:64] = 1e-39
+    if tokens > 30:
+        x[11, 5], x[12, 6], x[13, 7] = torch.nan, torch.inf, -torch.inf
+        x[14, 1:40] = -0.0
+        x[15] *= 1e-30
+        x[16, :32] = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0] * 4)[: min(32, cols)]   # ties
+        x[17] *= 1e34 if dtype == "fp32" else 1e30
+    x = x.to(DT[dtype])
+    n = tokens * k
+    width = cols if fmt == "e4m3" else (cols + 1) // 2
+    codes = torch.full((n, width), 0xA5, dtype=torch.uint8, device="cuda")
+    scales = torch.full((ops.scales_row_bytes(n, cols, 32, "mma"),), 0x5A, dtype=torch.uint8, device="cuda")
+    ops.mxfp4_moe_dispatch(x.cuda(), rows.cuda(), elem_format=fmt, scale_mode=mode, out=ops.DispatchResult(codes=codes, scales=scales))
+    bits = x.view(torch.int16).numpy().view(np.uint16) if dtype == "bf16" else x.numpy()
+    q = O.qdq8_rowwise(bits) if fmt == "e4m3" else O.qdq_rowwise(bits, 32, 6.0, O.SCALE_PAGE if mode == "page" else O.SCALE_FLOOR)
+    total = int((slots >= 0).sum())
+    token = (slots[:total].long() // k).numpy()
+    want = np.full((n, width), 0xA5, np.uint8)
+    want[:total] = q["codes"][token]
+    assert np.array_equal(codes.cpu().numpy(), want)
+    nblk = -(-cols // 32)
+    full = np.full((-(-n // 128) * 128, -(-nblk // 4) * 4), 0x5A, np.uint8)
+    full[n:] = 0                                   # padding is written as zero ...
+    full[:total, :nblk] = q["scales"][token]
+    full[:total, nblk:] = 0                        # ... also behind the last block of a written row
+    assert np.array_equal(scales.cpu().numpy(), O.mma_scale_layout(full).reshape(-1))
+
+
+@pytest.mark.parametrize("scale_factor", [1.0, 6.0, 20.0, 2.0 ** -70])
+def test_dispatch_scale_factors(scale_factor):
+    """The whole PAGE rule, also outside the range of the divide-free threshold."""
+    x = rnd(33, 256, seed=6, std=2.0, dtype=torch.bfloat16)
+    rows = torch.arange(33, dtype=torch.int32).view(33, 1)
+    r = ops.mxfp4_moe_dispatch(x.cuda(), rows.cuda(), emit_values=False, emit_codes=True, scale_factor=scale_factor)
+    q = O.qdq_rowwise(x.view(torch.int16).numpy().view(np.uint16), 32, scale_factor, O.SCALE_PAGE)
+    assert np.array_equal(r.codes.cpu().numpy(), q["codes"])
+    got = ops.mxfp4_qdq_fwd(x.cuda(), emit_codes=True, scale_factor=scale_factor, scales_layout="mma")
+    nb = 512 * 2
+    assert torch.equal(r.codes, got.codes_row) and torch.equal(r.scales[:nb], got.scales_row[:nb])
+
+
+def test_dispatch_every_bf16_value():
+    """Every bf16 value beside amaxes that put it in every binade of the format."""
+    v = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    v = v[torch.isfinite(v.float())]
+    rows_of = [v.float().abs().clamp(min=1e-37) * s for s in (1.0, 2.7, 5.0, 6.5)]
+    x = torch.cat([torch.stack([torch.cat([v[i:i + 1], a[i:i + 1].bfloat16()]).repeat(16) for i in range(0, v.numel(), 37)]) for a in rows_of])
+    x = x[torch.isfinite(x.float()).all(1)]
+    rows = torch.arange(x.shape[0], dtype=torch.int32).view(-1, 1)
+    for mode, code in (("page", O.SCALE_PAGE), ("floor", O.SCALE_FLOOR)):
+        r = ops.mxfp4_moe_dispatch(x.cuda(), rows.cuda(), emit_values=False, emit_codes=True, scale_mode=mode)
+        q = O.qdq_rowwise(x.view(torch.int16).numpy().view(np.uint16), 32, 6.0, code)
+        assert np.array_equal(r.codes.cpu().numpy(), q["codes"])
+
+
+def test_dispatch_skips_rows_outside_and_strides():
+    x = rnd(10, 100, seed=4, dtype=torch.bfloat16).cuda()[:, 1:97]
+    rows = torch.arange(20, dtype=torch.int32).view(10, 2)
+    rows[3, 1], rows[4, 0], rows[5, 0] = 20, -7, 2 ** 31 - 1
+    out = torch.zeros(20, 100, dtype=torch.bfloat16, device="cuda")[:, :96]
+    ops.mxfp4_moe_dispatch(x, rows.cuda(), out=ops.DispatchResult(values=out))
+    want = torch.zeros(20, 96, dtype=torch.bfloat16)
+    for t in range(10):
+        for j in range(2):
+            if 0 <= rows[t, j] < 20:
+                want[rows[t, j]] = x[t].cpu()
+    assert torch.equal(out.cpu(), want)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("tokens,k,cols", [(1, 1, 1), (4, 8, 64), (130, 6, 96), (67, 2, 1001), (19, 32, 40), (33, 4, 7168)])
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("weighted", [False, True])
+def test_combine(dtype, tokens, k, cols, residual, weighted):
+    """fp32 sums of k products (k roundings of the sums, k of the products
+    fused away) and the residual, then one rounding."""
+    rows, _, _ = a_plan(tokens, 40, k, seed=5, masked=0.2)
+    y = rnd(tokens * k, cols, seed=6, dtype=DT[dtype])
+    w = rnd(tokens, k, seed=7) if weighted else None
+    res = rnd(tokens, cols, seed=8, dtype=DT[dtype]) if residual else None
+    total = int((rows >= 0).sum())
+    y[total:] = torch.nan                           # rows no index names must not be read into a result
+    got = ops.mxfp4_moe_combine(y.cuda(), rows.cuda(), None if w is None else w.cuda(), residual=None if res is None else res.cuda())
+    some = (rows >= 0)[:, :, None]
+    picked = torch.where(some, y[rows.long().clamp(min=0)].double(), 0.0) * (1.0 if w is None else w.double()[:, :, None])
+    want = picked.sum(1) + (0.0 if res is None else res.double())
+    mag = picked.abs().sum(1) + (0.0 if res is None else res.double().abs())
+    close(got, want, (k + 2) * U32 * mag + (U16 if dtype == "bf16" else U32) * want.abs() * (1 + 2 ** -7), "combine")
+
+
+def test_combine_onto_its_residual():
+    rows, _, _ = a_plan(50, 8, 2)
+    y, w, res = rnd(100, 256, seed=1).cuda(), rnd(50, 2, seed=2).cuda(), rnd(50, 256, seed=3).cuda()
+    want = ops.mxfp4_moe_combine(y, rows.cuda(), w, residual=res)
+    got = ops.mxfp4_moe_combine(y, rows.cuda(), w, residual=res, out=res)
+    assert got is res and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("tokens,k,cols", [(1, 1, 1), (4, 8, 64), (130, 6, 96), (67, 2, 1001), (19, 32, 40), (33, 4, 7168)])
+def test_combine_backward(dtype, tokens, k, cols):
+    """grad_rows: one product, rounded to fp32 and to the type. grad_weights: a
+    thread sums its columns (of 256 threads' pieces), then 5 + 8 additions."""
+    rows, slots, _ = a_plan(tokens, 40, k, seed=5, masked=0.2)
+    y, g = rnd(tokens * k, cols, seed=6, dtype=DT[dtype]), rnd(tokens, cols, seed=9, dtype=DT[dtype])
+    w = rnd(tokens, k, seed=7)
+    out = torch.full((tokens * k, cols), 3.0, dtype=DT[dtype], device="cuda")
+    gy, gw = ops.mxfp4_moe_combine_bwd(g.cuda(), y.cuda(), rows.cuda(), w.cuda(), out=out)
+    total = int((slots >= 0).sum())
+    slot = slots[:total].long()
+    want = torch.full((tokens * k, cols), 3.0, dtype=torch.float64)
+    want[:total] = w.double().reshape(-1)[slot, None] * g.double()[slot // k]
+    close(gy, want, (U32 + (U16 if dtype == "bf16" else 0.0)) * want.abs() * (1 + 2 ** -7), "grad_rows")
+    prod = torch.where((rows >= 0)[:, :, None], y[rows.long().clamp(min=0)].double() * g.double()[:, None, :], 0.0)
+    chain = -(-cols // 256) + 16 + 13
+    close(gw, prod.sum(2), chain * U32 * prod.abs().sum(2), "grad_weights")
+    only = ops.mxfp4_moe_combine_bwd(g.cuda(), None, rows.cuda(), grad_weights=False, out=torch.zeros_like(out))
+    assert only[1] is None and torch.equal(only[0][:total].cpu(), g[slot // k])
+    only = ops.mxfp4_moe_combine_bwd(g.cuda(), y.cuda(), rows.cuda(), w.cuda(), grad_rows=False)
+    assert only[0] is None and torch.equal(only[1], gw)
+
+
+# ------------------------------------------------------------------------------- linear
+
+def operand(rows, k, fmt, seed, lo=126, hi=129):
+    g = gen(seed)
+    if fmt == "e2m1":
+        c = torch.randint(0, 256, (rows, k // 2), generator=g, dtype=torch.uint8)
+    else:
+        c = (torch.randn(rows, k, generator=g) * 80).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    nblk = k // 32
+    size = 512 * (-(-rows // 128)) * (-(-nblk // 4))
+    s = torch.full((size,), 0xFF, dtype=torch.uint8)       # scale padding is NaN: it must not be read as a scale
+    r = torch.arange(rows)[:, None]
+    b = torch.arange(nblk)[None, :]
+    at = 512 * ((r // 128) * (-(-nblk // 4)) + b // 4) + 16 * (r % 32) + 4 * (r % 128 // 32) + b % 4
+    s[at.reshape(-1)] = torch.randint(lo, hi, (rows * nblk,), generator=g, dtype=torch.uint8)
+    return c, s
+
+
+def linear_case(sizes, m, n, k, fmt, act="none", out="bf16", bias=False, residual=False, preact=False, list_type=1, seed=0, dense=False):
+    """One call against the product in 64 bits. Every product of two operand
+    values is exact in fp32; the K partial sums and the bias round (k + 1)
+    2^-24 of their magnitudes; an activation passes an error on with at most
+    its largest slope (1.13 for gelu; gated: the factors' sizes) and adds a few
+    fp32 roundings of its own value; then the residual and one rounding."""
+    g = len(sizes)
+    a, sa = operand(m, k, fmt, seed)
+    parts = [operand(n, k, fmt, seed + 1 + i, 117 if fmt == "e2m1" else 108, 119 if fmt == "e2m1" else 110) for i in range(g)]
+    b = torch.stack([p[0] for p in parts])
+    sb = torch.cat([p[1] for p in parts])
+    width = n // 2 if act == "swiglu" else n
+    dt = DT[out]
+    bv = rnd(g, n, seed=seed + 90) if bias else None
+    res = rnd(m, width, seed=seed + 91, dtype=dt) if residual else None
+    y0 = torch.full((m, width), 5.0, dtype=dt, device="cuda")
+    z0 = torch.full((m, n), 5.0, dtype=dt, device="cuda") if preact else None
+    gl = torch.tensor(sizes if list_type == 1 else np.cumsum(sizes), dtype=torch.int64, device="cuda")
+    r = ops.mxfp4_grouped_linear(a.cuda(), sa.cuda(), b.cuda(), sb.cuda(), None if dense else gl, k=k, elem_format=fmt,
+                                 group_list_type=list_type, bias=None if bv is None else bv.cuda(), activation=act,
+                                 residual=None if res is None else res.cuda(), out_dtype=dt,
+                                 out=ops.LinearResult(y=y0, preact=z0))
+    total = sum(sizes)
+    av = R.decode(a, sa, m, k, fmt)
+    z, mag = torch.zeros(total, n, dtype=torch.float64), torch.zeros(total, n, dtype=torch.float64)
+    first = 0
+    for i, size in enumerate(sizes):
+        w = R.decode(b[i], parts[i][1], n, k, fmt)
+        z[first:first + size] = av[first:first + size] @ w.T
+        mag[first:first + size] = av[first:first + size].abs() @ w.abs().T
+        if bv is not None:
+            z[first:first + size] += bv[i].double()
+            mag[first:first + size] += bv[i].double().abs()
+        first += size
+    ez = (k + 1) * U32 * mag
+    last = U16 if out == "bf16" else U32
+    want = R.activation(z, act)
+    if act == "swiglu":
+        gate, up, eg, eu = z[:, 0::2], z[:, 1::2], ez[:, 0::2], ez[:, 1::2]
+        ey = 1.1 * eg * (up.abs() + eu) + (gate.abs() + eg) * eu + 12 * U32 * (1 + gate.abs()) * want.abs()
+    else:
+        ey = 1.13 * ez + (0 if act in ("none", "relu") else 16) * U32 * (1 + z.abs()) * (want.abs() + U32)
+        if act == "gelu_tanh":     # its argument's rounding: 4 roundings of |u| <= 0.8 |z| (1 + 0.045 z^2), slope of the logistic 1/4
+            ey = ey + 8 * U32 * z.abs() * (1 + 0.1 * z ** 2) * torch.exp(-z.abs()).clamp(max=1.0) * z.abs()
+    if res is not None:
+        want = want + res[:total].double()
+        ey = ey + U32 * want.abs()
+    close(r.y[:total], want, ey + last * (want.abs() + ey), "y")
+    assert bool((r.y[total:] == 5.0).all())
+    if preact:
+        close(r.preact[:total], z, ez + last * (z.abs() + ez), "preact")
+        assert bool((r.preact[total:] == 5.0).all())
+    return r
+
+
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+@pytest.mark.parametrize("sizes,m", [([1], 1), ([0, 3, 0, 1, 1], 5), ([40, 0, 33, 7], 80), ([130, 65, 0, 200], 395), ([300], 300), ([0, 0], 9)])
+@pytest.mark.parametrize("n,k", [(64, 128), (200, 512), (130, 320), (513, 1088)])
+def test_linear_product(fmt, sizes, m, n, k):
+    linear_case(sizes, m, n, k, fmt)
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "gelu_tanh", "silu", "swiglu"])
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+@pytest.mark.parametrize("everything", [False, True])
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+def test_linear_epilogue(act, out, everything, fmt):
+    linear_case([20, 0, 150, 3], 180, 262, 256, fmt, act=act, out=out, bias=everything, residual=everything, preact=everything)
+
+
+@pytest.mark.parametrize("n", [1, 2, 31, 127, 128, 129, 255, 256, 257, 384, 385])
+def test_linear_widths(n):
+    linear_case([70, 9], 80, n, 192, "e2m1", out="fp32", bias=True, residual=True, preact=True)
+
+
+@pytest.mark.parametrize("k", [64, 128, 192, 256, 320, 576, 1024])
+def test_linear_lengths_e2m1(k):
+    linear_case([33, 5], 40, 140, k, "e2m1", out="fp32")
+
+
+@pytest.mark.parametrize("k", [32, 64, 96, 128, 160, 416, 1056])
+def test_linear_lengths_e4m3(k):
+    linear_case([33, 5], 40, 140, k, "e4m3", out="fp32")
+
+
+@pytest.mark.parametrize("sizes,m", [([5] * 30, 150), ([64] * 9, 576), ([200] * 5, 1000), ([0] * 50 + [700], 700)])
+def test_linear_many_tiles_per_cta(sizes, m):
+    """More tiles than SMs, in every token tile width."""
+    linear_case(sizes, m, 9000 if m < 700 else 7000, 128, "e2m1", act="swiglu", list_type=0)
+
+
+def test_linear_dense_and_views():
+    linear_case([77], 77, 300, 256, "e4m3", act="gelu", bias=True, residual=True, preact=True, dense=True)
+    # strided outputs and residual
+    a, sa = operand(50, 128, "e2m1", 1)
+    b, sb = operand(64, 128, "e2m1", 2)
+    res = rnd(50, 70, seed=3, dtype=torch.bfloat16).cuda()
+    y = torch.zeros(50, 99, dtype=torch.bfloat16, device="cuda")
+    plain = ops.mxfp4_grouped_linear(a.cuda(), sa.cuda(), b.cuda(), sb.cuda(), k=128, residual=res[:, 3:67].contiguous(), bias=rnd(64, seed=4).cuda())
+    ops.mxfp4_grouped_linear(a.cuda(), sa.cuda(), b.cuda(), sb.cuda(), k=128, residual=res[:, 3:67], bias=rnd(64, seed=4).cuda(),
+                             out=ops.LinearResult(y=y[:, 5:69]))
+    assert torch.equal(plain.y, y[:, 5:69]) and bool((y[:, :5] == 0).all()) and bool((y[:, 69:] == 0).all())
+
+
+def test_linear_agrees_with_the_grouped_gemm():
+    """Without an epilogue: the same product as mxfp4_grouped_gemm (both fp32 accumulations within the bound)."""
+    k, n, sizes = 512, 384, [100, 0, 250, 34]
+    a, sa = operand(sum(sizes), k, "e2m1", 5)
+    parts = [operand(n, k, "e2m1", 6 + i) for i in range(4)]
+    b, sb = torch.stack([p[0] for p in parts]).cuda(), torch.cat([p[1] for p in parts]).cuda()
+    gl = torch.tensor(sizes, dtype=torch.int64, device="cuda")
+    one = ops.mxfp4_grouped_gemm(a.cuda(), sa.cuda(), b, sb, gl, k=k, group_list_type=1)
+    two = ops.mxfp4_grouped_linear(a.cuda(), sa.cuda(), b, sb, gl, k=k, group_list_type=1, out_dtype=torch.float32).y
+    assert (one - two).norm() <= 2 * k * U32 * one.norm()
+
+
+def test_linear_invalid_lists():
+    a, sa = operand(50, 128, "e2m1", 1)
+    b, sb = operand(128, 128, "e2m1", 2)
+    args = (a.cuda(), sa.cuda(), b.view(2, 64, -1).cuda(), torch.cat([sb, sb]).cuda())
+    for sizes, kind in (([30, 21], 1), ([-1, 20], 1), ([40, 30], 0), ([10, 51], 0), ([2 ** 62, 2 ** 62], 1)):
+        gl = torch.tensor(sizes, dtype=torch.int64, device="cuda")
+        y = torch.full((50, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+        with pytest.raises(MXFP4ArgumentError):
+            ops.mxfp4_grouped_linear(*args, gl, k=128, group_list_type=kind, out=ops.LinearResult(y=y))
+        assert bool((y == 3.0).all())
+        r = ops.mxfp4_grouped_linear(*args, gl, k=128, group_list_type=kind, check=False)
+        assert int(r.status) == 1
+        with pytest.raises(MXFP4ArgumentError):
+            ops.mxfp4_grouped_linear_bwd(rnd(50, 64).cuda(), rnd(50, 64).cuda(), gl, group_list_type=kind)
+
+
+def test_linear_refusals():
+    a, sa = operand(50, 128, "e2m1", 1)
+    b, sb = operand(64, 128, "e2m1", 2)
+    a, sa, b, sb = a.cuda(), sa.cuda(), b.cuda(), sb.cuda()
+    ok = dict(k=128)
+    for bad in (dict(k=96), dict(k=0), dict(k=256), dict(activation="tanh"), dict(out_dtype=torch.float16), dict(elem_format="e5m2"),
+                dict(bias=torch.zeros(63, device="cuda")), dict(residual=torch.zeros(50, 63, device="cuda").bfloat16()),
+                dict(out=ops.LinearResult(y=torch.zeros(50, 63, device="cuda").bfloat16()))):
+        with pytest.raises((ValueError, TypeError)):
+            ops.mxfp4_grouped_linear(a, sa, b, sb, **{**ok, **bad})
+    with pytest.raises(ValueError):
+        ops.mxfp4_grouped_linear(a, sa[:100], b, sb, k=128)
+    with pytest.raises(ValueError):
+        ops.mxfp4_grouped_linear(a, sa, b, sb[:100], k=128)
+    with pytest.raises(ValueError):
+        ops.mxfp4_grouped_linear(a, sa, b[:63], sb, k=128, activation="swiglu")
+    with pytest.raises(ValueError):
+        ops.mxfp4_grouped_linear(a.t(), sa, b, sb, k=128)
+    with pytest.raises(TypeError):
+        ops.mxfp4_grouped_linear(a, sa, b, sb, k=128, bias=torch.zeros(64, device="cuda").bfloat16())
+
+
+def slope_bound(z, act):
+    """Rounding of a slope's evaluation: a few fp32 operations on terms of size 1 + |z|."""
+    return 24 * U32 * (1 + z.abs()) * (1.0 + (z ** 2).clamp(max=64.0) * (1.0 if act == "gelu_tanh" else 0.0))
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "gelu_tanh", "silu", "swiglu"])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("sizes,m,n", [([1], 1, 2), ([40, 0, 70, 1, 200], 320, 264), ([130], 130, 1026), ([0, 0], 5, 64), ([500, 12], 512, 4096)])
+def test_linear_backward(act, dtype, sizes, m, n):
+    """Against autograd of the activation in 64 bits; the bias sums add the
+    unrounded gradients (64 rows by 8 warps, 8 warps, then the units in order)."""
+    width = n // 2 if act == "swiglu" else n
+    z = rnd(m, n, seed=1, std=2.0, dtype=DT[dtype])
+    gy = rnd(m, width, seed=2, dtype=DT[dtype])
+    gl = torch.tensor(sizes, dtype=torch.int64, device="cuda")
+    out = torch.full((m, n), 9.0, dtype=DT[dtype], device="cuda")
+    gz, gb = ops.mxfp4_grouped_linear_bwd(gy.cuda(), z.cuda(), gl, group_list_type=1, activation=act, out=out)
+    total = sum(sizes)
+    v = z.double().requires_grad_(True)
+    (want,) = torch.autograd.grad(R.activation(v, act), v, gy.double())
+    if act == "swiglu":
+        e = torch.empty_like(want)
+        gate, up, g = z.double()[:, 0::2], z.double()[:, 1::2], gy.double().abs()
+        e[:, 0::2] = slope_bound(gate, act) * g * up.abs()
+        e[:, 1::2] = slope_bound(gate, act) * g
+    else:
+        e = slope_bound(z.double(), act) * gy.double().abs() if act not in ("none", "relu") else U32 * want.abs()
+    close(gz[:total], want[:total], e[:total] + (U16 if dtype == "bf16" else U32) * (want.abs() + e)[:total], "grad_preact")
+    assert bool((gz[total:] == 9.0).all())
+    first = 0
+    for i, size in enumerate(sizes):
+        part = want[first:first + size]
+        chain = 8 + 8 + size // 64 + 1
+        close(gb[i], part.sum(0), e[first:first + size].sum(0) + chain * U32 * part.abs().sum(0), "grad_bias")
+        first += size
+    none = ops.mxfp4_grouped_linear_bwd(gy.cuda(), z.cuda(), gl, group_list_type=1, activation=act, bias_grad=False, out=torch.zeros_like(out))
+    assert none[1] is None and torch.equal(none[0][:total], gz[:total])
+
+
+def test_linear_backward_large_values():
+    z = torch.tensor([[-3e38, -1e20, -100.0, -20.0, 20.0, 100.0, 1e20, 3e38]]).cuda()
+    g = torch.ones(1, 8).cuda()
+    for act in ("relu", "gelu", "gelu_tanh", "silu"):
+        gz, gb = ops.mxfp4_grouped_linear_bwd(g, z, activation=act)
+        want = torch.tensor([[0.0, 0, 0, 0, 1, 1, 1, 1]])
+        close(gz, want.double(), 1e-6, act)
+        assert torch.equal(gb.cpu(), gz.cpu())
+
+
+def test_linear_backward_strided():
+    z, g = rnd(70, 100, seed=1).cuda(), rnd(70, 60, seed=2).cuda()
+    one = ops.mxfp4_grouped_linear_bwd(g[:, 7:53], z[:, 3:95], activation="swiglu")
+    two = ops.mxfp4_grouped_linear_bwd(g[:, 7:53].contiguous(), z[:, 3:95].contiguous(), activation="swiglu")
+    assert torch.equal(one[0], two[0])
+    # other threads hold the columns, the sums' order is the same
+    assert torch.equal(one[1], two[1])
+
+
+# ------------------------------------------------------------------ as they are used together
+
+def layer(x, router, w1, s1, w2, s2, hidden, k, mask=None, check=False):
+    """A quantised mixture-of-experts layer: route, dispatch quantised, gated
+    product, quantise, product, combine onto the input."""
+    experts = router.shape[1]
+    t, cols = x.shape
+    r = ops.mxfp4_moe_route(x.float() @ router, k, score="sigmoid", num_groups=2, topk_groups=1, token_mask=mask)
+    d = ops.mxfp4_moe_dispatch(x, r.rows, emit_values=False, emit_codes=True)
+    h = ops.mxfp4_grouped_linear(d.codes, d.scales, w1, s1, r.counts, k=cols, group_list_type=1, activation="swiglu", check=check)
+    q = ops.mxfp4_qdq_fwd(h.y, emit_values=False, emit_codes=True, scales_layout="mma")
+    y = ops.mxfp4_grouped_linear(q.codes_row, q.scales_row, w2, s2, r.counts, k=hidden, group_list_type=1, check=check)
+    return ops.mxfp4_moe_combine(y.y, r.rows, r.weights, residual=x), r
+
+
+def a_layer(t, cols=256, hidden=128, experts=8, seed=0):
+    x = rnd(t, cols, seed=seed, dtype=torch.bfloat16).cuda()
+    router = rnd(cols, experts, seed=seed + 1, std=0.1).cuda()
+    w1 = rnd(experts, 2 * hidden, cols, seed=seed + 2, std=0.06, dtype=torch.bfloat16)
+    w2 = rnd(experts, cols, hidden, seed=seed + 3, std=0.08, dtype=torch.bfloat16)
+    ops1 = [ops.mxfp4_mma_operand(w.cuda()) for w in w1]
+    ops2 = [ops.mxfp4_mma_operand(w.cuda()) for w in w2]
+    pack = lambda o: (torch.stack([c.view(torch.uint8) for c, _ in o]), torch.cat([s.view(torch.uint8) for _, s in o]))  # noqa: E731
+    return x, router, pack(ops1), pack(ops2), w1, w2
+
+
+def layer_plain(x, r, w1, w2, k):
+    """The layer on the oracle's fake-quantised values, in 64 bits but for the
+    bf16 roundings between its steps."""
+    bits = lambda v: v.contiguous().view(torch.int16).numpy().view(np.uint16)  # noqa: E731
+    q = lambda v: torch.from_numpy(O.bf16_to_f32(O.qdq_rowwise(bits(v), 32, 6.0, O.SCALE_PAGE)["y"])).double()  # noqa: E731
+    out = x.double()
+    qx = q(x)
+    qw1 = [q(w) for w in w1]
+    qw2 = [q(w) for w in w2]
+    for t in range(x.shape[0]):
+        for j in range(k):
+            e = int(r.experts[t, j])
+            if e < 0:
+                continue
+            h = R.activation((qx[t:t + 1] @ qw1[e].T), "swiglu").bfloat16()
+            y = (q(h) @ qw2[e].T).bfloat16().double()
+            out[t] += float(r.weights[t, j]) * y[0]
+    return out
+
+
+@pytest.mark.parametrize("tokens", [1, 5, 70])
+def test_layer(tokens):
+    k = 3
+    x, router, (w1, s1), (w2, s2), f1, f2 = a_layer(tokens)
+    mask = torch.ones(tokens, dtype=torch.bool, device="cuda")
+    if tokens > 3:
+        mask[2] = False
+    out, r = layer(x, router, w1, s1, w2, s2, 128, k, mask)
+    want = layer_plain(x.cpu(), r, f1, f2, k)
+    if tokens > 3:
+        assert torch.equal(out[2], x[2])
+    # an intermediate that rounds the other way moves one code by at most a step: the result as a whole stays near
+    assert (out.double().cpu() - want).norm() <= 2 * U16 * want.norm()
+
+
+def test_layer_in_a_graph_and_on_streams():
+    """Captured and replayed on new inputs, two graphs in turn, and two streams at once: the results of the eager calls."""
+    k = 3
+    x, router, (w1, s1), (w2, s2), _, _ = a_layer(130)
+    xs = [rnd(130, 256, seed=40 + i, dtype=torch.bfloat16).cuda() for i in range(3)]
+    want = [layer(v, router, w1, s1, w2, s2, 128, k)[0] for v in xs]
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        static = x.clone()
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            layer(static, router, w1, s1, w2, s2, 128, k)
+        torch.cuda.current_stream().wait_stream(side)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out, _ = layer(static, router, w1, s1, w2, s2, 128, k)
+        graphs.append((g, static, out))
+    for v, w in zip(xs, want):
+        for g, static, out in graphs:
+            static.copy_(v)
+            g.replay()
+            assert torch.equal(out, w)
+    for g, static, out in graphs:   # one after the other without waiting in between
+        static.copy_(xs[1])
+        g.replay()
+    assert torch.equal(graphs[0][2], want[1]) and torch.equal(graphs[1][2], want[1])
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    outs = []
+    for s, v in zip(streams, xs):
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            outs.append([layer(v, router, w1, s1, w2, s2, 128, k)[0] for _ in range(4)])
+    torch.cuda.synchronize()
+    for w, got in zip(want, outs):
+        assert all(torch.equal(w, o) for o in got)
+
+
+def test_training_step_of_a_layer():
+    """Forward and backward through the operators (dispatch of values, product,
+    combine, router) against autograd of the same layer in 64 bits."""
+    t, cols, n, experts, k = 90, 128, 192, 6, 2
+    x = rnd(t, cols, seed=1)
+    lg = rnd(t, experts, seed=2)
+    bias = rnd(experts, n, seed=4)
+    go = rnd(t, n, seed=5)
+    r = ops.mxfp4_moe_route(lg.cuda(), k)
+    rows, chosen = r.rows.cpu(), r.experts.cpu()
+    # fp32 values so that only fp32 roundings separate the two; the product is formed on quantised copies
+    d = ops.mxfp4_moe_dispatch(x.cuda(), r.rows, emit_values=True, emit_codes=True, elem_format="e4m3", scale_mode="floor")
+    w = [operand(n, cols, "e4m3", 20 + e, 108, 110) for e in range(experts)]
+    b, sb = torch.stack([c for c, _ in w]).cuda(), torch.cat([s for _, s in w]).cuda()
+    h = ops.mxfp4_grouped_linear(d.codes, d.scales, b, sb, r.counts, k=cols, elem_format="e4m3", group_list_type=1, bias=bias.cuda(),
+                                 activation="gelu", out_dtype=torch.float32, emit_preact=True)
+    out = ops.mxfp4_moe_combine(h.y, r.rows, r.weights)
+    gy, gw = ops.mxfp4_moe_combine_bwd(go.cuda(), h.y, r.rows, r.weights)
+    gz, gb = ops.mxfp4_grouped_linear_bwd(gy, h.preact, r.counts, group_list_type=1, activation="gelu")
+    gl = ops.mxfp4_moe_route_bwd(gw, lg.cuda(), r.experts)
+    # the same in 64 bits, from the quantised rows
+    qx = R.decode(d.codes.cpu(), d.scales.cpu(), t * k, cols, "e4m3")
+    lgd, bd = lg.double().requires_grad_(True), bias.double().requires_grad_(True)
+    weights = R.route_weights(lgd, chosen, "softmax", True, 1.0)
+    order = torch.empty(t * k, dtype=torch.long)
+    order[rows.reshape(-1).long()] = torch.arange(t * k)
+    expert = chosen.reshape(-1).long()[order]
+    wd = torch.stack([R.decode(c, s, n, cols, "e4m3") for c, s in w])
+    z = torch.einsum("rk,rnk->rn", qx, wd[expert]) + bd[expert]
+    z.retain_grad()
+    y = R.activation(z, "gelu")
+    want = (weights.reshape(-1)[:, None] * y[rows.reshape(-1).long()]).view(t, k, n).sum(1)
+    want.backward(go.double())
+    for got, ref in ((out, want), (gz, z.grad), (gb, bd.grad), (gl, lgd.grad)):
+        # norms: each is a chain of fp32 steps whose products have 128 terms
+        assert (got.double().cpu() - ref).norm() <= 512 * U32 * ref.norm()
+    # the dispatch's gradient is a combine without weights
+    gx = ops.mxfp4_moe_combine(d.values, r.rows)
+    assert torch.equal(gx.cpu(), k * x)
