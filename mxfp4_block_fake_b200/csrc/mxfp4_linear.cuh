@@ -158,7 +158,9 @@ __device__ int64_t ln_plan(const Args& a, int32_t* s_tpre, int32_t* s_rst)
 
 // ---- activations -----------------------------------------------------------
 
-__device__ __forceinline__ float act_sigmoid(float z) { return 1.0f / (1.0f + expf(-z)); }
+// 1 / (1 + e^-z) by the approximate exponential and quotient: their errors, a few
+// 2^-23 plus |z| 2^-24 relative, are of the order of z's own rounding.
+__device__ __forceinline__ float act_sigmoid(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
 
 // act(z) of the elementwise activations. gelu_tanh: 0.5 z (1 + tanh u) is z
 // times the logistic function of 2u; gelu: 0.5 z erfc(-z / sqrt 2), which does
@@ -218,42 +220,142 @@ __device__ __forceinline__ void ln_store(void* p, int64_t i, float v)
         static_cast<uint16_t*>(p)[i] = (uint16_t)f32_to_bf16(v);
 }
 
-// 32 tokens of this thread's feature: v[i] = z of token row0 + i.
-template <bool F32>
-__device__ __forceinline__ void ln_epilogue32(const LnArgs& a, float (&v)[32], int64_t row0, int rows, int f, bool fok)
+// One activation, chosen at compile time where a loop holds many of them.
+template <int ACT>
+__device__ __forceinline__ float act_of(float z)
 {
-    if (a.preact && fok) {
+    return act_value(z, ACT);
+}
+
+// 32 tokens of this thread's feature: v[i] = z of token i of `rows`. The
+// pointers are those of token 0 and this thread's column (the activated
+// width's where the activation is gated). Loads of the residual go ahead of
+// the stores eight tokens at a time, since y may be the residual.
+template <int ACT, bool F32>
+__device__ __forceinline__ void ln_finish32(const float (&v)[32], int rows, bool fok, char* y, int64_t ld_y,
+                                            const char* res, int64_t ld_res)
+{
+    constexpr int ESZ = F32 ? 4 : 2;
+    constexpr bool GATED = ACT == MXFP4_ACT_SWIGLU;
+    constexpr int STEP = GATED ? 2 : 1;
+    // gated: lanes 2j and 2j + 1 hold gate j and up j; of a pair of tokens the
+    // even lane finishes the first, the odd lane the second
+    const bool odd = GATED && (threadIdx.x & 1);
+    const int first = odd ? 1 : 0;
+    y += first * ld_y * ESZ;
+    if (res)
+        res += first * ld_res * ESZ;
+#pragma unroll
+    for (int i0 = 0; i0 < 32; i0 += 8 * STEP) {
+        float o[8];
+        if (res) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                o[i] = fok && i0 + STEP * i + first < rows ? ln_load<F32>(res + (int64_t)(i0 + STEP * i) * ld_res * ESZ, 0) : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float a;
+            if constexpr (GATED) {
+                const int t = i0 + 2 * i;
+                const float other = __shfl_xor_sync(FULL, odd ? v[t] : v[t + 1], 1);
+                const float gate = odd ? other : v[t], up = odd ? v[t + 1] : other;
+                a = act_of<MXFP4_ACT_SILU>(gate) * up;
+            } else {
+                a = act_of<ACT>(v[i0 + i]);
+            }
+            o[i] = res ? a + o[i] : a;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (fok && i0 + STEP * i + first < rows)
+                ln_store<F32>(y + (int64_t)(i0 + STEP * i) * ld_y * ESZ, 0, o[i]);
+    }
+}
+
+template <bool F32>
+__device__ __forceinline__ void ln_epilogue32(const LnArgs& a, const float (&v)[32], int64_t row0, int rows, int f, bool fok)
+{
+    constexpr int ESZ = F32 ? 4 : 2;
+    if (a.preact) {
+        char* z = static_cast<char*>(a.preact) + (row0 * a.ld_z + f) * ESZ;
 #pragma unroll
         for (int i = 0; i < 32; ++i)
-            if (i < rows)
-                ln_store<F32>(a.preact, (row0 + i) * a.ld_z + f, v[i]);
+            if (fok && i < rows)
+                ln_store<F32>(z + (int64_t)i * a.ld_z * ESZ, 0, v[i]);
     }
-    if (a.act == MXFP4_ACT_SWIGLU) {
-        // lanes 2j and 2j + 1 hold gate j and up j: of a pair of tokens the even
-        // lane finishes the first, the odd lane the second
-        const bool odd = threadIdx.x & 1;
+    const int fo = a.act == MXFP4_ACT_SWIGLU ? f >> 1 : f;
+    char* y = static_cast<char*>(a.y) + (row0 * a.ld_y + fo) * ESZ;
+    const char* res = a.residual ? static_cast<const char*>(a.residual) + (row0 * a.ld_res + fo) * ESZ : nullptr;
+    // the branch is outside the loops: one activation's code runs
+    switch (a.act) {
+    case MXFP4_ACT_NONE:
+        return ln_finish32<MXFP4_ACT_NONE, F32>(v, rows, fok, y, a.ld_y, res, a.ld_res);
+    case MXFP4_ACT_RELU:
+        return ln_finish32<MXFP4_ACT_RELU, F32>(v, rows, fok, y, a.ld_y, res, a.ld_res);
+    case MXFP4_ACT_GELU:
+        return ln_finish32<MXFP4_ACT_GELU, F32>(v, rows, fok, y, a.ld_y, res, a.ld_res);
+    case MXFP4_ACT_GELU_TANH:
+        return ln_finish32<MXFP4_ACT_GELU_TANH, F32>(v, rows, fok, y, a.ld_y, res, a.ld_res);
+    case MXFP4_ACT_SILU:
+        return ln_finish32<MXFP4_ACT_SILU, F32>(v, rows, fok, y, a.ld_y, res, a.ld_res);
+    default:
+        return ln_finish32<MXFP4_ACT_SWIGLU, F32>(v, rows, fok, y, a.ld_y, res, a.ld_res);
+    }
+}
+
+// True in one lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
+// Low word of a shared-memory descriptor: the address in units of 16 bytes and
+// a leading byte offset of 16. Advancing the address adds to this word.
+__device__ __forceinline__ uint32_t ln_desc_lo(uint32_t saddr) { return ((saddr >> 4) & 0x3FFFu) | (1u << 16); }
+// High words: operands (8-row groups 1024 bytes apart, version 1, 128-byte
+// swizzle) and scale atoms (core matrices 128 bytes apart, no swizzle).
+constexpr uint32_t LN_OPERAND_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t LN_SCALE_HI = (128u >> 4) | (1u << 14);
+
+__device__ __forceinline__ uint64_t ln_desc(uint32_t lo, uint32_t hi) { return ((uint64_t)hi << 32) | lo; }
+
+// One stage: its scale atoms into tensor memory, then its MMAs (up to 4 along
+// K for NH halves of the features). Straight-line for a full stage: a single
+// thread issues all of it, so every address must be at hand.
+template <int FMT, int NT, int NH>
+__device__ __forceinline__ void ln_stage(uint32_t d_tmem, uint32_t sf_col, uint32_t wlo, uint32_t xlo, uint32_t sfw,
+                                         uint32_t sfx, int na, int nk, bool accumulate)
+{
+    using F = LnFmt<FMT>;
+    constexpr int ATOMS = F::ATOMS;
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-            const float other = __shfl_xor_sync(FULL, odd ? v[i] : v[i + 1], 1);
-            const float gate = odd ? other : v[i], up = odd ? v[i + 1] : other;
-            float o = gate * act_sigmoid(gate) * up;
-            const int tok = i + (odd ? 1 : 0);
-            if (fok && tok < rows) {
-                if (a.residual)
-                    o += ln_load<F32>(a.residual, (row0 + tok) * a.ld_res + (f >> 1));
-                ln_store<F32>(a.y, (row0 + tok) * a.ld_y + (f >> 1), o);
-            }
-        }
-        return;
+    for (int i = 0; i < ATOMS; ++i) {
+        if (i > 0 && i >= na)
+            break;
+#pragma unroll
+        for (int h = 0; h < NH; ++h)
+            asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(sf_col + 4u * (2 * i + h)),
+                         "l"(ln_desc(sfw + (uint32_t)(512 / 16) * (ATOMS * h + i), LN_SCALE_HI))
+                         : "memory");
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(sf_col + 4u * (2 * ATOMS + i)),
+                     "l"(ln_desc(sfx + (uint32_t)(512 / 16) * i, LN_SCALE_HI))
+                     : "memory");
     }
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        if (fok && i < rows) {
-            float o = act_value(v[i], a.act);
-            if (a.residual)
-                o += ln_load<F32>(a.residual, (row0 + i) * a.ld_res + f);
-            ln_store<F32>(a.y, (row0 + i) * a.ld_y + f, o);
-        }
+    for (int kk = 0; kk < 4; ++kk) {
+        if (kk > 0 && kk >= nk)
+            break;
+        // 32 bytes of K per MMA; its first scale block is byte (block % 4) of atom (block / 4)
+        constexpr int SB = F::MMA_K / 32;
+        const uint32_t ai = (uint32_t)((kk * SB) >> 2);
+#pragma unroll
+        for (int h = 0; h < NH; ++h)
+            gm_mma<FMT>(d_tmem + (uint32_t)(h * NT), ln_desc(wlo + (uint32_t)(h * 128 * LN_ROW_BYTES / 16 + 2 * kk), LN_OPERAND_HI),
+                        ln_desc(xlo + 2u * kk, LN_OPERAND_HI), ln_idesc(F::AB_FMT, (uint32_t)((kk * SB) & 3), NT),
+                        sf_col + 4u * (2 * ai + h), sf_col + 4u * (2 * ATOMS + ai), kk > 0 || accumulate ? 1u : 0u);
     }
 }
 
@@ -364,69 +466,58 @@ __global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_cons
                     (void)mbar_wait(smem_addr(&sm.full[i]), i < s ? ph : ph ^ 1u);
         __syncwarp();
     } else if (warp == 1) {
-        // ---- MMA issuer (lane 0)
-        if (lane == 0) {
-            int s = 0, acc = 0;
-            uint32_t ph = 0, aph = 0;
-            for (int64_t t = blockIdx.x; t < tiles && !sm.err; t += gridDim.x) {
-                const LnTile tl = ln_tile<NT>(a, s_tpre, s_rst, t, n_ft);
-                if (!mbar_wait(smem_addr(&sm.acc_empty[acc]), aph ^ 1u)) {
+        // ---- MMA issuer. The whole warp walks the tiles, so that addresses and
+        // descriptors stay in uniform registers; one elected lane issues.
+        int s = 0, acc = 0;
+        uint32_t ph = 0, aph = 0;
+        for (int64_t t = blockIdx.x; t < tiles && !sm.err; t += gridDim.x) {
+            const LnTile tl = ln_tile<NT>(a, s_tpre, s_rst, t, n_ft);
+            if (!__all_sync(FULL, mbar_wait(smem_addr(&sm.acc_empty[acc]), aph ^ 1u))) {
+                sm.err = 1;
+                break;
+            }
+            gm_fence_after();
+            const uint32_t d_tmem = tmem + (uint32_t)(acc * 2 * NT);
+            for (int ks = 0; ks < nst; ++ks) {
+                if (!__all_sync(FULL, mbar_wait(smem_addr(&sm.full[s]), ph))) {
                     sm.err = 1;
                     break;
                 }
                 gm_fence_after();
-                const uint32_t d_tmem = tmem + (uint32_t)(acc * 2 * NT);
-                for (int ks = 0; ks < nst; ++ks) {
-                    if (!mbar_wait(smem_addr(&sm.full[s]), ph)) {
-                        sm.err = 1;
-                        break;
-                    }
-                    gm_fence_after();
-                    // the tokens' scales were written by the producer's copies
-                    // (generic proxy); tcgen05.cp reads them in the async proxy
-                    fence_async_smem();
+                // the tokens' scales were written by the producer's copies
+                // (generic proxy); tcgen05.cp reads them in the async proxy
+                fence_async_smem();
+                if (elect_one()) {
                     const uint32_t sf_col = tmem + SM::SF_COL0 + (uint32_t)(12 * ATOMS * s);
+                    const uint32_t wlo = ln_desc_lo(smem_addr(sm.w[s])), xlo = ln_desc_lo(smem_addr(sm.x[s]));
                     const int na = (int)min((int64_t)ATOMS, ncb - (int64_t)ks * ATOMS);
-#pragma unroll
-                    for (int i = 0; i < ATOMS; ++i) {
-                        if (i >= na)
-                            break;
-                        for (int h = 0; h < tl.nh; ++h)
-                            asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(sf_col + 4u * (2 * i + h)),
-                                         "l"(gm_sf_desc(smem_addr(sm.sfw[s][h]) + 512 * i))
-                                         : "memory");
-                        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(sf_col + 4u * (2 * ATOMS + i)),
-                                     "l"(gm_sf_desc(smem_addr(sm.sfx[s]) + 512 * i))
-                                     : "memory");
-                    }
-                    const uint64_t wd = gm_smem_desc(smem_addr(sm.w[s]), 2, 1024);
-                    const uint64_t xd = gm_smem_desc(smem_addr(sm.x[s]), 2, 1024);
-                    const int nk = min(4, nmma - 4 * ks);
-                    for (int kk = 0; kk < nk; ++kk) {
-                        // 32 bytes of K per MMA; its first scale block is byte (block % 4) of atom (block / 4)
-                        const int blk = kk * (F::MMA_K / 32);
-                        const uint32_t ai = (uint32_t)(blk >> 2);
-                        const uint32_t id = ln_idesc(F::AB_FMT, (uint32_t)(blk & 3), NT);
-                        for (int h = 0; h < tl.nh; ++h)
-                            gm_mma<FMT>(d_tmem + h * NT, wd + (uint64_t)(h * 128 * LN_ROW_BYTES / 16) + 2u * kk, xd + 2u * kk, id,
-                                        sf_col + 4u * (2 * ai + h), sf_col + 4u * (2 * ATOMS + ai), (ks > 0 || kk > 0) ? 1u : 0u);
-                    }
+                    const int nk = nmma - 4 * ks;
+                    if (tl.nh == 2)
+                        ln_stage<FMT, NT, 2>(d_tmem, sf_col, wlo, xlo, ln_desc_lo(smem_addr(sm.sfw[s][0])),
+                                             ln_desc_lo(smem_addr(sm.sfx[s])), na, nk, ks > 0);
+                    else
+                        ln_stage<FMT, NT, 1>(d_tmem, sf_col, wlo, xlo, ln_desc_lo(smem_addr(sm.sfw[s][0])),
+                                             ln_desc_lo(smem_addr(sm.sfx[s])), na, nk, ks > 0);
                     gm_commit(smem_addr(&sm.empty[s]));
-                    if (++s == S) {
-                        s = 0;
-                        ph ^= 1u;
-                    }
+                    if (ks + 1 == nst)
+                        gm_commit(smem_addr(&sm.acc_full[acc]));
                 }
-                gm_commit(smem_addr(&sm.acc_full[acc]));
-                if (++acc == NACC) {
-                    acc = 0;
-                    aph ^= 1u;
+                __syncwarp();
+                if (++s == S) {
+                    s = 0;
+                    ph ^= 1u;
                 }
             }
-            // every MMA issued has completed before the tensor memory is freed
-            gm_commit(smem_addr(&sm.done));
-            (void)mbar_wait(smem_addr(&sm.done), 0);
+            if (++acc == NACC) {
+                acc = 0;
+                aph ^= 1u;
+            }
         }
+        // every MMA issued has completed before the tensor memory is freed
+        if (elect_one())
+            gm_commit(smem_addr(&sm.done));
+        __syncwarp();
+        (void)mbar_wait(smem_addr(&sm.done), 0);
         __syncwarp();
     } else {
         // ---- epilogue: tensor-memory lanes 32 (warp % 4) .. + 31 of half h
