@@ -22,9 +22,12 @@
 //     an atom).
 //   warp 1: copies the scale atoms into tensor memory (tcgen05.cp) and issues
 //     the block-scaled MMAs.
-//   warps 2-9: epilogue, four per half. A warp reads its 32 features of every
-//     token from tensor memory into registers, hands the accumulator back, and
-//     then does its arithmetic and stores while the next tile is multiplied.
+//   the other warps: epilogue, four per half and 64 tokens. A warp reads its 32
+//     features of its tokens from tensor memory into registers, hands the
+//     accumulator back, and then does its arithmetic and stores while the next
+//     tile is multiplied. (With 128 tokens per warp the values no longer fit
+//     the registers beside the arithmetic: 347 against 172 us on 32768 x 4096 x
+//     1024, swiglu.)
 // Every wait on an mbarrier is bounded (SG_WAIT_NS); on expiry the CTA records
 // MXFP4_ECUDA, waits (bounded) for its loads and MMAs in flight, frees the
 // tensor memory and exits.
@@ -32,7 +35,6 @@
 namespace mxfp4 {
 
 constexpr int LN_FT = 256;              // features per tile
-constexpr int LN_THREADS = 320;         // producer, MMA, 8 epilogue warps
 constexpr uint32_t LN_TMEM_COLS = 512;
 constexpr int LN_ROW_BYTES = 128;       // bytes of an operand row per stage
 
@@ -58,6 +60,9 @@ struct __align__(1024) LnSmem {
     static constexpr int ATOMS = LnFmt<FMT>::ATOMS;
     static constexpr int S = 4;                    // stages (227 KB with the plan of MAX_GROUPS groups)
     static constexpr int NACC = NT > 64 ? 1 : 2;   // accumulators in tensor memory
+    static constexpr int TW = NT < 64 ? NT : 64;   // tokens of an epilogue warp
+    static constexpr int EPI_WARPS = 8 * (NT / TW);
+    static constexpr int THREADS = 64 + 32 * EPI_WARPS;
     static constexpr uint32_t SF_COL0 = NACC * 2 * NT;
     // groups whose plan (two words each) fits beside the stages
     static constexpr int MAX_GROUPS = NT > 64 ? 2048 : MXFP4_MAX_GROUPS;
@@ -231,7 +236,7 @@ __device__ __forceinline__ float act_of(float z)
 // pointers are those of token 0 and this thread's column (the activated
 // width's where the activation is gated). Loads of the residual go ahead of
 // the stores eight tokens at a time, since y may be the residual.
-template <int ACT, bool F32>
+template <int ACT, bool F32, bool WHOLE>
 __device__ __forceinline__ void ln_finish32(const float (&v)[32], int rows, bool fok, char* y, int64_t ld_y,
                                             const char* res, int64_t ld_res)
 {
@@ -250,8 +255,10 @@ __device__ __forceinline__ void ln_finish32(const float (&v)[32], int rows, bool
         float o[8];
         if (res) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                o[i] = fok && i0 + STEP * i + first < rows ? ln_load<F32>(res + (int64_t)(i0 + STEP * i) * ld_res * ESZ, 0) : 0.0f;
+            for (int i = 0; i < 8; ++i) {
+                o[i] = WHOLE || (fok && i0 + STEP * i + first < rows) ? ln_load<F32>(res, 0) : 0.0f;
+                res += ld_res * (STEP * ESZ);
+            }
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -267,22 +274,26 @@ __device__ __forceinline__ void ln_finish32(const float (&v)[32], int rows, bool
             o[i] = res ? a + o[i] : a;
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (fok && i0 + STEP * i + first < rows)
-                ln_store<F32>(y + (int64_t)(i0 + STEP * i) * ld_y * ESZ, 0, o[i]);
+        for (int i = 0; i < 8; ++i) {
+            if (WHOLE || (fok && i0 + STEP * i + first < rows))
+                ln_store<F32>(y, 0, o[i]);
+            y += ld_y * (STEP * ESZ);
+        }
     }
 }
 
-template <bool F32>
+template <bool F32, bool WHOLE>
 __device__ __forceinline__ void ln_epilogue32(const LnArgs& a, const float (&v)[32], int64_t row0, int rows, int f, bool fok)
 {
     constexpr int ESZ = F32 ? 4 : 2;
     if (a.preact) {
         char* z = static_cast<char*>(a.preact) + (row0 * a.ld_z + f) * ESZ;
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (fok && i < rows)
-                ln_store<F32>(z + (int64_t)i * a.ld_z * ESZ, 0, v[i]);
+        for (int i = 0; i < 32; ++i) {
+            if (WHOLE || (fok && i < rows))
+                ln_store<F32>(z, 0, v[i]);
+            z += a.ld_z * ESZ;
+        }
     }
     const int fo = a.act == MXFP4_ACT_SWIGLU ? f >> 1 : f;
     char* y = static_cast<char*>(a.y) + (row0 * a.ld_y + fo) * ESZ;
@@ -290,17 +301,17 @@ __device__ __forceinline__ void ln_epilogue32(const LnArgs& a, const float (&v)[
     // the branch is outside the loops: one activation's code runs
     switch (a.act) {
     case MXFP4_ACT_NONE:
-        return ln_finish32<MXFP4_ACT_NONE, F32>(v, rows, fok, y, a.ld_y, res, a.ld_res);
+        return ln_finish32<MXFP4_ACT_NONE, F32, WHOLE>(v, rows, fok, y, a.ld_y, res, a.ld_res);
     case MXFP4_ACT_RELU:
-        return ln_finish32<MXFP4_ACT_RELU, F32>(v, rows, fok, y, a.ld_y, res, a.ld_res);
+        return ln_finish32<MXFP4_ACT_RELU, F32, WHOLE>(v, rows, fok, y, a.ld_y, res, a.ld_res);
     case MXFP4_ACT_GELU:
-        return ln_finish32<MXFP4_ACT_GELU, F32>(v, rows, fok, y, a.ld_y, res, a.ld_res);
+        return ln_finish32<MXFP4_ACT_GELU, F32, WHOLE>(v, rows, fok, y, a.ld_y, res, a.ld_res);
     case MXFP4_ACT_GELU_TANH:
-        return ln_finish32<MXFP4_ACT_GELU_TANH, F32>(v, rows, fok, y, a.ld_y, res, a.ld_res);
+        return ln_finish32<MXFP4_ACT_GELU_TANH, F32, WHOLE>(v, rows, fok, y, a.ld_y, res, a.ld_res);
     case MXFP4_ACT_SILU:
-        return ln_finish32<MXFP4_ACT_SILU, F32>(v, rows, fok, y, a.ld_y, res, a.ld_res);
+        return ln_finish32<MXFP4_ACT_SILU, F32, WHOLE>(v, rows, fok, y, a.ld_y, res, a.ld_res);
     default:
-        return ln_finish32<MXFP4_ACT_SWIGLU, F32>(v, rows, fok, y, a.ld_y, res, a.ld_res);
+        return ln_finish32<MXFP4_ACT_SWIGLU, F32, WHOLE>(v, rows, fok, y, a.ld_y, res, a.ld_res);
     }
 }
 
@@ -360,7 +371,7 @@ __device__ __forceinline__ void ln_stage(uint32_t d_tmem, uint32_t sf_col, uint3
 }
 
 template <int FMT, int NT, bool F32>
-__global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_constant__ LnMaps maps, const LnArgs a)
+__global__ void __launch_bounds__(LnSmem<FMT, NT>::THREADS, 1) linear_kernel(const __grid_constant__ LnMaps maps, const LnArgs a)
 {
     using F = LnFmt<FMT>;
     using SM = LnSmem<FMT, NT>;
@@ -380,7 +391,7 @@ __global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_cons
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&sm.acc_full[i]), 1);
-            mbar_init(smem_addr(&sm.acc_empty[i]), 8);
+            mbar_init(smem_addr(&sm.acc_empty[i]), SM::EPI_WARPS);
         }
         mbar_init(smem_addr(&sm.done), 1);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -520,8 +531,10 @@ __global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_cons
         (void)mbar_wait(smem_addr(&sm.done), 0);
         __syncwarp();
     } else {
-        // ---- epilogue: tensor-memory lanes 32 (warp % 4) .. + 31 of half h
-        const int quad = warp & 3, h = (warp - 2) >> 2;
+        // ---- epilogue: tensor-memory lanes 32 (warp % 4) .. + 31 of half h,
+        // tokens c0 .. c0 + TW - 1 of the tile
+        constexpr int TW = SM::TW;
+        const int quad = warp & 3, h = ((warp - 2) >> 2) & 1, c0 = ((warp - 2) >> 3) * TW;
         int acc = 0;
         uint32_t aph = 0;
         for (int64_t t = blockIdx.x; t < tiles && !sm.err; t += gridDim.x) {
@@ -534,12 +547,12 @@ __global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_cons
                 break;
             }
             gm_fence_after();
-            float v[NT / 32][32];
+            float v[TW / 32][32];
 #pragma unroll
-            for (int c = 0; c < NT / 32; ++c) {
+            for (int c = 0; c < TW / 32; ++c) {
                 uint32_t u[32];
                 __syncwarp();
-                gm_ld32(tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)(acc * 2 * NT + h * NT + 32 * c), u);
+                gm_ld32(tmem + ((uint32_t)(32 * quad) << 16) + (uint32_t)(acc * 2 * NT + h * NT + c0 + 32 * c), u);
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                     v[c][i] = __uint_as_float(u[i]) + bias;
@@ -554,13 +567,18 @@ __global__ void __launch_bounds__(LN_THREADS, 1) linear_kernel(const __grid_cons
             }
             if (h < tl.nh) {
 #pragma unroll 1
-                for (int c = 0; c < NT / 32; ++c) {
-                    if (32 * c >= tl.rows)
+                for (int c = 0; c < TW / 32; ++c) {
+                    const int rows = tl.rows - c0 - 32 * c;
+                    if (rows <= 0)
                         break;
-                    ln_epilogue32<F32>(a, v[0], tl.row0 + 32 * c, tl.rows - 32 * c, f, fok);
+                    // whole chunks (every lane a feature, 32 tokens) take no predicates
+                    if (rows >= 32 && __all_sync(FULL, fok))
+                        ln_epilogue32<F32, true>(a, v[0], tl.row0 + c0 + 32 * c, rows, f, fok);
+                    else
+                        ln_epilogue32<F32, false>(a, v[0], tl.row0 + c0 + 32 * c, rows, f, fok);
                     // the next 32 tokens move up, so that the code exists once
 #pragma unroll
-                    for (int d = 0; d + 1 < NT / 32; ++d)
+                    for (int d = 0; d + 1 < TW / 32; ++d)
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
                             v[d][i] = v[d + 1][i];

@@ -314,7 +314,7 @@ static mxfp4_status launch_linear_t(const LnMaps& maps, const LnArgs& g, cudaStr
     LnMaps m = maps;
     LnArgs a = g;
     void* args[] = {&m, &a};
-    return launched(cudaLaunchKernel(fn, dim3((unsigned)(bound < sms ? bound : sms)), dim3(LN_THREADS), args, smem, s));
+    return launched(cudaLaunchKernel(fn, dim3((unsigned)(bound < sms ? bound : sms)), dim3(SM::THREADS), args, smem, s));
 }
 
 template <int FMT, int NT>
