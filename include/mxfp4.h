@@ -556,7 +556,13 @@ typedef struct mxfp4_moe_move_args {
     void* grad_rows;
     int64_t ld_grad_rows;
     float* grad_weights;
+    void* workspace;          /* dispatch of codes: optional, see below */
+    int64_t workspace_bytes;
 } mxfp4_moe_move_args;
+
+/* Bytes of workspace (4-byte aligned) with which a large dispatch of codes lays
+ * its scales out faster; 0 where it would not. Without it the result is the same. */
+int64_t mxfp4_moe_dispatch_workspace(int64_t tokens, int32_t k, int64_t cols, int64_t row_count);
 
 mxfp4_status mxfp4_moe_dispatch(const mxfp4_moe_move_args* args, mxfp4_stream_t stream);
 mxfp4_status mxfp4_moe_combine(const mxfp4_moe_move_args* args, mxfp4_stream_t stream);

@@ -42,6 +42,7 @@ EXPORTS = (
     "mxfp4_moe_route_workspace",
     "mxfp4_moe_route",
     "mxfp4_moe_route_bwd",
+    "mxfp4_moe_dispatch_workspace",
     "mxfp4_moe_dispatch",
     "mxfp4_moe_combine",
     "mxfp4_moe_combine_bwd",
@@ -185,6 +186,8 @@ class MoveArgs(ctypes.Structure):
         ("grad_rows", ctypes.c_void_p),
         ("ld_grad_rows", ctypes.c_int64),
         ("grad_weights", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_int64),
     ]
 
 
@@ -273,6 +276,8 @@ def lib() -> ctypes.CDLL:
     L.mxfp4_dual_level_qdq.restype = i32
     L.mxfp4_moe_route_workspace.argtypes = [i64, i64]
     L.mxfp4_moe_route_workspace.restype = i64
+    L.mxfp4_moe_dispatch_workspace.argtypes = [i64, i32, i64, i64]
+    L.mxfp4_moe_dispatch_workspace.restype = i64
     L.mxfp4_grouped_linear_workspace.argtypes = [i64, i64, i64]
     L.mxfp4_grouped_linear_workspace.restype = i64
     for name, struct in (("mxfp4_moe_route", RouteArgs), ("mxfp4_moe_route_bwd", RouteArgs),

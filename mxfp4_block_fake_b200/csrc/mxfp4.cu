@@ -258,14 +258,6 @@ __device__ __forceinline__ void rare_fixup(const QP& p, int e, uint32_t (&ob)[VE
 
 // ---- bf16 fast path: two elements per 32-bit word ---------------------------
 
-// Packed unsigned 16-bit max of two words.
-__device__ __forceinline__ uint32_t vmax2(uint32_t a, uint32_t b)
-{
-    uint32_t r;
-    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
 // A block takes the bf16 fast path when 2^-126 <= 2^k <= 2^16. k <= 16 keeps
 // every nonzero bf16 x clear of the fp32 underflow of x / 2^k (|x| >= 2^-133
 // > 2^(k-150)), so sign(y) is the sign of x; k >= -126 keeps 2^k normal, so

@@ -343,6 +343,14 @@ __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.a
 // Row-wise bf16 block-32 quantisation core
 // ---------------------------------------------------------------------------
 
+// Packed unsigned 16-bit max of two words.
+__device__ __forceinline__ uint32_t vmax2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 // Block exponent for a scale mode fixed at compile time (block_k's rule).
 template <int MODE>
 __device__ __forceinline__ int block_kt(uint32_t A, uint32_t thr)

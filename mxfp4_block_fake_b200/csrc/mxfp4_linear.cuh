@@ -599,12 +599,15 @@ __global__ void __launch_bounds__(LnSmem<FMT, NT>::THREADS, 1) linear_kernel(con
 // ---------------------------------------------------------------------------
 // Gradients of the epilogue: dz = dy act'(z) (gated: d gate = dy up silu'(gate),
 // d up = dy silu(gate)), dbias_g = the sum of dz over the group's rows, in
-// fp32 from the unrounded dz. A CTA takes LB_ROWS rows of one group by 32
-// threads' columns; partial sums go to ws[unit][n], and a second kernel adds a
-// group's units in order.
+// fp32 from the unrounded dz. Bound by memory. A CTA takes LB_ROWS rows of one
+// group by a stretch of columns as wide as its threads reach (2048 bf16
+// columns; narrower matrices take several rows side by side), so that it reads
+// and writes long pieces of a row at a time, LB_UNROLL rows in flight. Partial
+// sums (a thread's rows in order, then the rows side by side) go to
+// ws[unit][n], and a second kernel adds a group's units in order.
 // ---------------------------------------------------------------------------
 
-constexpr int LB_ROWS = 64;
+constexpr int LB_ROWS = 32;
 
 struct LnBwdArgs {
     const void* grad;      // [m][ld_g]
@@ -616,26 +619,94 @@ struct LnBwdArgs {
     int32_t* status;
     int64_t m, n, ld_g, ld_z, ld_dz;
     int32_t num_groups, gl_type, act;
+    int32_t across_log2;   // log2 of a row's threads
 };
 
+// PER columns of one row of z and the matching gradients, as loaded (the
+// vector form keeps 16-byte words until they are used: registers bound how many
+// rows are in flight) and as fp32.
+template <int ESZ, bool VEC, int PER>
+struct LbPiece {
+    uint4 z;
+    uint4 g;   // gated: the low half
+
+    __device__ __forceinline__ void load(const LnBwdArgs& a, int64_t row, int64_t c, bool gated)
+    {
+        z = g = make_uint4(0u, 0u, 0u, 0u);
+        if (c >= a.n)
+            return;
+        if constexpr (VEC) {
+            z = ld_stream(static_cast<const char*>(a.z) + (row * a.ld_z + c) * ESZ);
+            if (gated) {
+                const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const char*>(a.grad) + (row * a.ld_g + (c >> 1)) * ESZ);
+                g.x = q.x;
+                g.y = q.y;
+            } else {
+                g = ld_stream(static_cast<const char*>(a.grad) + (row * a.ld_g + c) * ESZ);
+            }
+        } else {  // two columns, one element a word
+            z.x = mv_load<ESZ>(a.z, row * a.ld_z + c);
+            g.x = mv_load<ESZ>(a.grad, row * a.ld_g + (gated ? c >> 1 : c));
+            if (c + 1 < a.n) {
+                z.y = mv_load<ESZ>(a.z, row * a.ld_z + c + 1);
+                if (!gated)
+                    g.y = mv_load<ESZ>(a.grad, row * a.ld_g + c + 1);
+            }
+        }
+    }
+
+    static __device__ __forceinline__ void spread(const uint4& q, float (&v)[PER])
+    {
+        const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            if constexpr (VEC && ESZ == 2)
+                v[i] = __uint_as_float(i & 1 ? u[i / 2] & 0xFFFF0000u : u[i / 2] << 16);
+            else
+                v[i] = __uint_as_float(u[i] << (ESZ == 2 ? 16 : 0));
+        }
+    }
+};
+
+template <int PER>
+__device__ __forceinline__ void lb_slope(const LnBwdArgs& a, bool gated, const float (&z)[PER], const float (&g)[PER], float (&d)[PER])
+{
+    if (gated) {
+#pragma unroll
+        for (int i = 0; i < PER; i += 2) {
+            const float gate = z[i], s = act_sigmoid(gate);
+            d[i] = g[i / 2] * z[i + 1] * (s * (1.0f + gate * (1.0f - s)));
+            d[i + 1] = g[i / 2] * (gate * s);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+            d[i] = g[i] * act_slope(z[i], a.act);
+    }
+}
+
+constexpr int LB_UNROLL = 2;
+
 template <int ESZ, bool VEC>
-__global__ void __launch_bounds__(NTHREADS) linear_bwd_kernel(const LnBwdArgs a)
+__global__ void __launch_bounds__(NTHREADS, 4) linear_bwd_kernel(const LnBwdArgs a)
 {
     constexpr int PER = VEC ? 16 / ESZ : 2;   // columns of z per thread
-    constexpr int WARPS = NTHREADS / 32;
     extern __shared__ __align__(16) int32_t lb_dyn[];
-    __shared__ float s_sum[WARPS][32 * PER];
+    __shared__ float s_sum[NTHREADS * PER];
     int32_t* s_tpre = lb_dyn;
     int32_t* s_rst = lb_dyn + a.num_groups + 1;
     const int64_t units = ln_plan<LB_ROWS>(a, s_tpre, s_rst);
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x;
     if (blockIdx.x == 0 && tid == 0 && a.status)
         *a.status = units >= 0 ? MXFP4_OK : MXFP4_EINVAL;
-    const int64_t n_ct = (a.n + 32 * PER - 1) / (32 * PER);
     const bool gated = a.act == MXFP4_ACT_SWIGLU;
+    const int across = 1 << a.across_log2;             // threads along a row
+    const int down = NTHREADS >> a.across_log2;        // rows side by side
+    const int64_t n_ct = (a.n + (int64_t)across * PER - 1) / (across * PER);
+    const int tc = tid & (across - 1), tr = tid >> a.across_log2;
     for (int64_t w = blockIdx.x; w < (units < 0 ? 0 : units * n_ct); w += gridDim.x) {
         const uint32_t unit = (uint32_t)(w / n_ct);
-        const int64_t c = (w - (int64_t)unit * n_ct) * 32 * PER + lane * PER;
+        const int64_t c0 = (w - (int64_t)unit * n_ct) * across * PER, c = c0 + (int64_t)tc * PER;
         int lo = 0, hi = a.num_groups - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
@@ -650,82 +721,52 @@ __global__ void __launch_bounds__(NTHREADS) linear_bwd_kernel(const LnBwdArgs a)
 #pragma unroll
         for (int i = 0; i < PER; ++i)
             sum[i] = 0.0f;
-        for (int r = warp; r < nr; r += WARPS) {
-            const int64_t row = r0 + r;
-            float z[PER], g[PER];
+        for (int r = tr; r < nr; r += LB_UNROLL * down) {
+            LbPiece<ESZ, VEC, PER> in[LB_UNROLL];
 #pragma unroll
-            for (int i = 0; i < PER; ++i)
-                z[i] = g[i] = 0.0f;
-            if constexpr (VEC) {
-                if (c < a.n) {
-                    piece_load<ESZ, PER>(a.z, row * a.ld_z + c, z);
-                    if (!gated) {
-                        piece_load<ESZ, PER>(a.grad, row * a.ld_g + c, g);
+            for (int q = 0; q < LB_UNROLL; ++q)
+                if (r + q * down < nr)
+                    in[q].load(a, r0 + r + q * down, c, gated);
+#pragma unroll
+            for (int q = 0; q < LB_UNROLL; ++q)
+                if (r + q * down < nr) {
+                    const int64_t row = r0 + r + q * down;
+                    float z[PER], g[PER], d[PER];
+                    in[q].spread(in[q].z, z);
+                    in[q].spread(in[q].g, g);
+                    lb_slope<PER>(a, gated, z, g, d);
+#pragma unroll
+                    for (int i = 0; i < PER; ++i)
+                        sum[i] += d[i];
+                    if constexpr (VEC) {
+                        if (c < a.n)
+                            piece_store<ESZ, PER>(a.grad_z, row * a.ld_dz + c, d);
                     } else {
-                        const uint2 q = *reinterpret_cast<const uint2*>(static_cast<const char*>(a.grad) + (row * a.ld_g + (c >> 1)) * ESZ);
-                        if constexpr (ESZ == 2) {
-                            g[0] = __uint_as_float(q.x << 16);
-                            g[1] = __uint_as_float(q.x & 0xFFFF0000u);
-                            g[2] = __uint_as_float(q.y << 16);
-                            g[3] = __uint_as_float(q.y & 0xFFFF0000u);
-                        } else {
-                            g[0] = __uint_as_float(q.x);
-                            g[1] = __uint_as_float(q.y);
-                        }
+#pragma unroll
+                        for (int i = 0; i < PER; ++i)
+                            if (c + i < a.n)
+                                ln_store<ESZ == 4>(a.grad_z, row * a.ld_dz + c + i, d[i]);
                     }
                 }
-            } else {
+        }
+        if (a.grad_bias) {
+            if (down > 1) {
 #pragma unroll
                 for (int i = 0; i < PER; ++i)
-                    if (c + i < a.n) {
-                        z[i] = ln_load<ESZ == 4>(a.z, row * a.ld_z + c + i);
-                        if (!gated)
-                            g[i] = ln_load<ESZ == 4>(a.grad, row * a.ld_g + c + i);
-                    }
-                if (gated && c < a.n)
-                    g[0] = ln_load<ESZ == 4>(a.grad, row * a.ld_g + (c >> 1));
+                    s_sum[(tr * across + tc) * PER + i] = sum[i];
+                __syncthreads();
+                if (tr == 0)
+                    for (int q = 1; q < down; ++q)
+#pragma unroll
+                        for (int i = 0; i < PER; ++i)
+                            sum[i] += s_sum[(q * across + tc) * PER + i];
+                __syncthreads();
             }
-            float d[PER];
-            if (gated) {
-#pragma unroll
-                for (int i = 0; i < PER; i += 2) {
-                    const float gate = z[i], s = act_sigmoid(gate);
-                    d[i] = g[i / 2] * z[i + 1] * (s * (1.0f + gate * (1.0f - s)));
-                    d[i + 1] = g[i / 2] * (gate * s);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < PER; ++i)
-                    d[i] = g[i] * act_slope(z[i], a.act);
-            }
-#pragma unroll
-            for (int i = 0; i < PER; ++i)
-                sum[i] += d[i];
-            if constexpr (VEC) {
-                if (c < a.n)
-                    piece_store<ESZ, PER>(a.grad_z, row * a.ld_dz + c, d);
-            } else {
+            if (tr == 0)
 #pragma unroll
                 for (int i = 0; i < PER; ++i)
                     if (c + i < a.n)
-                        ln_store<ESZ == 4>(a.grad_z, row * a.ld_dz + c + i, d[i]);
-            }
-        }
-        if (a.grad_bias) {
-#pragma unroll
-            for (int i = 0; i < PER; ++i)
-                s_sum[warp][lane * PER + i] = sum[i];
-            __syncthreads();
-            const int64_t c0 = (w - (int64_t)unit * n_ct) * 32 * PER;
-            for (int i = tid; i < 32 * PER; i += NTHREADS) {
-                float v = 0.0f;
-#pragma unroll
-                for (int q = 0; q < WARPS; ++q)
-                    v += s_sum[q][i];
-                if (c0 + i < a.n)
-                    a.ws[(int64_t)unit * a.n + c0 + i] = v;
-            }
-            __syncthreads();
+                        a.ws[(int64_t)unit * a.n + c + i] = sum[i];
         }
     }
 }

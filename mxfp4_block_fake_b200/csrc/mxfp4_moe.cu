@@ -24,10 +24,41 @@ namespace mxfp4 {
 
 static mxfp4_status launched(cudaError_t e) { return e == cudaSuccess ? MXFP4_OK : MXFP4_ECUDA; }
 
+// Lets `fn` be launched with `smem` bytes of dynamic shared memory; asked of the
+// runtime once per (kernel, device) and size above the last.
+static bool allow_smem(const void* fn, size_t smem)
+{
+    if (smem <= 48 * 1024)
+        return true;
+    struct Entry {
+        const void* fn;
+        int dev;
+        size_t smem;
+    };
+    static Entry cache[128];
+    static int n = 0;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess)
+        return false;
+    std::lock_guard<std::mutex> lk(g_mu);
+    int i = 0;
+    while (i < n && !(cache[i].fn == fn && cache[i].dev == dev))
+        ++i;
+    if (i < n && cache[i].smem >= smem)
+        return true;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return false;
+    if (i < 128) {
+        cache[i] = Entry{fn, dev, smem};
+        n = i < n ? n : i + 1;
+    }
+    return true;
+}
+
 template <typename A>
 static mxfp4_status launch1(const void* fn, int64_t grid, int threads, size_t smem, const A& arg, cudaStream_t s)
 {
-    if (smem > 48 * 1024 && cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    if (!allow_smem(fn, smem))
         return MXFP4_ECUDA;
     A a = arg;
     void* args[] = {&a};
@@ -190,7 +221,7 @@ static mxfp4_status run_dispatch(const mxfp4_moe_move_args* A, cudaStream_t s)
         if (e4 && A->scale_mode != MXFP4_SCALE_FLOOR)
             return MXFP4_EUNSUPPORTED;
     }
-    if (A->cols == 0 || (A->tokens > 0 && A->row_count > 0 && (!A->x || !aligned(A->x, esz) || !aligned(A->values, esz))))
+    if (A->cols == 0 || (A->tokens > 0 && A->row_count > 0 && (!A->x || !aligned(A->x, esz) || !aligned(A->values, esz) || !aligned(A->workspace, 4))))
         return A->cols == 0 ? MXFP4_OK : MXFP4_EINVAL;
     DispatchArgs a;
     memset(&a, 0, sizeof(a));
@@ -218,12 +249,31 @@ static mxfp4_status run_dispatch(const mxfp4_moe_move_args* A, cudaStream_t s)
     }
     if (A->codes && st == MXFP4_OK) {
         const int64_t npad = ((A->cols + 31) / 32 + 3) & ~(int64_t)3;
-        const void* fn = esz == 2 ? (e4 ? (const void*)dispatch_quant_kernel<2, MXFP4_ELEM_E4M3> : (const void*)dispatch_quant_kernel<2, MXFP4_ELEM_E2M1>)
+        const bool stream = A->cols % 32 == 0 && aligned(A->x, 32) && (A->ld_tokens * (int64_t)esz) % 32 == 0 &&
+                            aligned(A->codes, 32) && aligned(A->scales, 4) && A->tokens * npad < INT32_MAX;
+        a.thr = !e4 && A->scale_mode == MXFP4_SCALE_PAGE && page_fast_ok(A->scale_factor) ? page_threshold(A->scale_factor) : 0u;
+        const void* fn = stream ? (esz == 2 ? (e4 ? (const void*)dispatch_stream_kernel<2, MXFP4_ELEM_E4M3> : (const void*)dispatch_stream_kernel<2, MXFP4_ELEM_E2M1>)
+                                            : (e4 ? (const void*)dispatch_stream_kernel<4, MXFP4_ELEM_E4M3> : (const void*)dispatch_stream_kernel<4, MXFP4_ELEM_E2M1>))
+                       : esz == 2 ? (e4 ? (const void*)dispatch_quant_kernel<2, MXFP4_ELEM_E4M3> : (const void*)dispatch_quant_kernel<2, MXFP4_ELEM_E2M1>)
                                   : (e4 ? (const void*)dispatch_quant_kernel<4, MXFP4_ELEM_E4M3> : (const void*)dispatch_quant_kernel<4, MXFP4_ELEM_E2M1>);
-        if (work)
-            st = launch_stride(fn, A->tokens * npad, a, s);
-        if (st == MXFP4_OK && A->row_count % 128 != 0)
-            st = launch_stride((const void*)pad_scale_kernel, (128 - A->row_count % 128) * npad, a, s);
+        const int64_t pad = A->row_count % 128 != 0 ? (128 - A->row_count % 128) * npad : 0;
+        const int64_t units = work ? A->tokens * npad : 0;
+        if (!work)
+            a.tokens = 0;
+        const int64_t ws = mxfp4_moe_dispatch_workspace(A->tokens, A->k, A->cols, A->row_count);
+        const bool staged = stream && work && ws > 0 && A->workspace && A->workspace_bytes >= ws;
+        if (staged) {
+            a.ws_scales = static_cast<uint32_t*>(A->workspace);
+            a.ws_pair = reinterpret_cast<int32_t*>(a.ws_scales + A->tokens * (npad / 4));
+        }
+        if (units > 0 || pad > 0)
+            st = launch_stride(fn, units > pad ? units : pad, a, s);
+        if (st == MXFP4_OK && staged) {
+            DispatchArgs arg = a;
+            void* args[] = {&arg};
+            const dim3 grid((unsigned)((A->row_count + 127) / 128), (unsigned)((npad / 4 + SG_WORDS - 1) / SG_WORDS));
+            st = launched(cudaLaunchKernel((const void*)dispatch_scales_kernel, grid, dim3(NTHREADS), args, 0, s));
+        }
     }
     return st;
 }
@@ -305,7 +355,7 @@ static mxfp4_status launch_linear_t(const LnMaps& maps, const LnArgs& g, cudaStr
     using SM = LnSmem<FMT, NT>;
     const void* fn = (const void*)linear_kernel<FMT, NT, F32>;
     const size_t smem = sizeof(SM) + 1024 + (size_t)(2 * (g.num_groups + 1)) * sizeof(int32_t);
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    if (!allow_smem(fn, smem))
         return MXFP4_ECUDA;
     const int sms = device_sms();
     if (sms <= 0)
@@ -462,7 +512,10 @@ static mxfp4_status run_linear_bwd(const mxfp4_linear_args* A, cudaStream_t s)
     const int sms = device_sms(), occ = occupancy(fn, plan);
     if (sms <= 0 || occ <= 0)
         return MXFP4_ECUDA;
-    const int64_t ct = 32 * (vec ? per : 2);
+    b.across_log2 = 5;
+    while (b.across_log2 < 8 && ((int64_t)(vec ? per : 2) << b.across_log2) < A->n)
+        ++b.across_log2;
+    const int64_t ct = (int64_t)(vec ? per : 2) << b.across_log2;
     const int64_t units = (A->m / LB_ROWS + groups) * ((A->n + ct - 1) / ct), most = (int64_t)sms * occ;
     st = launch1(fn, units < most ? units : most, NTHREADS, plan, b, s);
     if (st == MXFP4_OK && A->grad_bias) {
@@ -496,6 +549,16 @@ mxfp4_status mxfp4_moe_route(const mxfp4_moe_route_args* args, mxfp4_stream_t st
 mxfp4_status mxfp4_moe_route_bwd(const mxfp4_moe_route_args* args, mxfp4_stream_t stream)
 {
     return run_route_bwd(args, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int64_t mxfp4_moe_dispatch_workspace(int64_t tokens, int32_t k, int64_t cols, int64_t row_count)
+{
+    if (tokens < 0 || k < 1 || cols < 0 || row_count < 0)
+        return -1;
+    // by 4-byte stores the scales cost about 8 us per million words, the second
+    // kernel about 3 us and a sixth of that
+    const int64_t words = (cols + 127) / 128;
+    return tokens * k * words < (int64_t)1 << 19 ? 0 : (tokens * words + row_count) * 4;
 }
 
 mxfp4_status mxfp4_moe_dispatch(const mxfp4_moe_move_args* args, mxfp4_stream_t stream)

@@ -18,6 +18,8 @@ struct DispatchArgs {
     uint8_t* scales;       // MMA layout of [out_rows][blocks]
     int64_t tokens, cols, ld, ld_y, out_rows;
     int64_t code_ld;       // bytes of a code row
+    uint32_t* ws_scales;   // [tokens][block columns / 4] scale words, or NULL: scales are written directly
+    int32_t* ws_pair;      // [out_rows]: the (token, slot) whose row this is, unless the rows say otherwise
     float sf;
     uint32_t thr;          // PAGE mode threshold (page_threshold)
     int32_t k, mode;
@@ -63,6 +65,16 @@ __global__ void __launch_bounds__(NTHREADS) dispatch_values_kernel(const Dispatc
             }
         }
     }
+}
+
+// Zeros in the scale rows behind the last one (the rest of the last atom row).
+__device__ __forceinline__ void pad_scale_rows(const DispatchArgs& a)
+{
+    const int64_t nblk = (a.cols + 31) / 32, npad = (nblk + 3) & ~(int64_t)3;
+    const int64_t last = (a.out_rows + 127) & ~(int64_t)127;
+    const int64_t n = (last - a.out_rows) * npad;
+    for (int64_t i = (int64_t)blockIdx.x * NTHREADS + threadIdx.x; i < n; i += (int64_t)gridDim.x * NTHREADS)
+        a.scales[srow_off_mma(a.out_rows + i / npad, i % npad, nblk)] = 0;
 }
 
 // Quantised rows, any width and alignment: one thread per (token, block of
@@ -121,19 +133,208 @@ __global__ void __launch_bounds__(NTHREADS) dispatch_quant_kernel(const Dispatch
             a.scales[srow_off_mma(r, b, nblk)] = (uint8_t)e8;
         }
     }
+    pad_scale_rows(a);
 }
 
-// Zeros in the scale rows behind the last one (the rest of the last atom row).
-__device__ __forceinline__ void pad_scale_rows(const DispatchArgs& a)
+// A block of 32 fp32 values (bits) -> its codes: E2M1 nibbles of 8 elements
+// per word (4 words), E4M3 bytes of 4 per word (8 words). E2M1: the hardware
+// convert rounds to nearest with ties to even, the codebook sends ties up; a
+// tie is one of the fp32 values with at most two fraction bits, so those get
+// one more in their last place first, which moves codes themselves nowhere.
+// y + 0 turns -0 into +0 (the codebook's sign rule).
+template <int FMT, int N>
+__device__ __forceinline__ void quant_block(const uint32_t (&x)[32], const BP& p, uint32_t (&code)[N])
 {
-    const int64_t nblk = (a.cols + 31) / 32, npad = (nblk + 3) & ~(int64_t)3;
-    const int64_t last = (a.out_rows + 127) & ~(int64_t)127;
-    const int64_t n = (last - a.out_rows) * npad;
-    for (int64_t i = (int64_t)blockIdx.x * NTHREADS + threadIdx.x; i < n; i += (int64_t)gridDim.x * NTHREADS)
-        a.scales[srow_off_mma(a.out_rows + i / npad, i % npad, nblk)] = 0;
+    if constexpr (FMT == MXFP4_ELEM_E4M3) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float y[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                y[j] = __fmul_rn(__uint_as_float(x[4 * i + j]), p.inv);
+            uint16_t lo, hi;
+            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(y[1]), "f"(y[0]));
+            asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(y[3]), "f"(y[2]));
+            code[i] = p.nanm ? 0u : (uint32_t)lo | (uint32_t)hi << 16;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float y[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const uint32_t b = __float_as_uint(__fmaf_rn(__uint_as_float(x[8 * i + j]), p.inv, 0.0f));
+                y[j] = __uint_as_float(b | ((b & 0x1FFFFFu) == 0u ? 1u : 0u));
+            }
+            uint32_t w;
+            asm("{\n\t.reg .b8 q0, q1, q2, q3;\n\t"
+                "cvt.rn.satfinite.e2m1x2.f32 q0, %2, %1;\n\t"
+                "cvt.rn.satfinite.e2m1x2.f32 q1, %4, %3;\n\t"
+                "cvt.rn.satfinite.e2m1x2.f32 q2, %6, %5;\n\t"
+                "cvt.rn.satfinite.e2m1x2.f32 q3, %8, %7;\n\t"
+                "mov.b32 %0, {q0, q1, q2, q3};\n\t}"
+                : "=r"(w)
+                : "f"(y[0]), "f"(y[1]), "f"(y[2]), "f"(y[3]), "f"(y[4]), "f"(y[5]), "f"(y[6]), "f"(y[7]));
+            code[i] = p.nanm ? 0u : w;
+        }
+    }
 }
 
-__global__ void __launch_bounds__(NTHREADS) pad_scale_kernel(const DispatchArgs a) { pad_scale_rows(a); }
+// Quantised rows of whole blocks (cols % 32 == 0, 32-byte aligned rows, fewer
+// than 2^31 blocks): one thread per (token, block), its 32 values by 32-byte
+// loads, its codes to each of the k rows by one 16- or 32-byte store, and the
+// scale bytes of four neighbouring blocks (the four lanes of a quad, a row's
+// whole atom entry) as one word, the k rows shared out among the quad's lanes.
+// Bound by memory: it reads x once and writes k rows of codes. bf16 blocks in
+// the usual exponent range take the streaming quantiser's convert (nibs4_cvt).
+template <int ESZ, int FMT>
+__global__ void __launch_bounds__(NTHREADS) dispatch_stream_kernel(const DispatchArgs a)
+{
+    constexpr int NC = FMT == MXFP4_ELEM_E4M3 ? 8 : 4;  // code words of a block
+    const uint32_t nblk = (uint32_t)(a.cols / 32), npad = (nblk + 3) & ~3u;
+    constexpr int NW = 8 * ESZ;                         // words of a block
+    const uint32_t total = (uint32_t)a.tokens * npad, stride = gridDim.x * NTHREADS;
+    auto load = [&](uint32_t v, uint32_t (&w)[NW]) {
+        const uint32_t t = v / npad, b = v - t * npad;
+        if (b < nblk) {
+            const char* xp = static_cast<const char*>(a.x) + ((int64_t)t * a.ld + 32 * b) * ESZ;
+#pragma unroll
+            for (int i = 0; i < NW / 8; ++i)
+                ld_nc_v8(xp + 32 * i, w + 8 * i);
+        }
+    };
+    uint32_t w[NW];
+    uint32_t u = blockIdx.x * NTHREADS + threadIdx.x;
+    if (u < total)
+        load(u, w);
+    for (; u < total; u += stride) {
+        const uint32_t t = u / npad, b = u - t * npad;
+        const unsigned quad = 0xFu << (threadIdx.x & 28);
+        const int32_t* rp = a.rows + (int64_t)t * a.k;
+        uint32_t wn[NW];
+        const bool more = u + stride < total;
+        if (more)
+            load(u + stride, wn);  // the next block's loads are in flight while this one is worked on
+        uint32_t code[NC], e8 = 0;
+        if (b < nblk) {
+            if constexpr (ESZ == 2) {
+                uint32_t m2 = 0;
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    m2 = vmax2(m2, w[i] & 0x7FFF7FFFu);
+                const uint32_t A = max(m2 & 0xFFFFu, m2 >> 16) << 16;
+                bool done = false;
+                if constexpr (FMT == MXFP4_ELEM_E2M1) {
+                    if (a.thr || a.mode == MXFP4_SCALE_FLOOR) {
+                        const int k = a.mode == MXFP4_SCALE_FLOOR ? block_kt<MXFP4_SCALE_FLOOR>(A, 0u) : block_kt<MXFP4_SCALE_PAGE>(A, a.thr);
+                        if (k_fast_bf(k) && A < 0x7F800000u) {
+                            const float invn = inv_nudged(k);
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+                                code[c] = nibs4_cvt(w + 4 * c, invn);
+                            e8 = (uint32_t)(k + 127);
+                            done = true;
+                        }
+                    }
+                }
+                if (!done) {
+                    uint32_t x[32];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        x[2 * i] = w[i] << 16;
+                        x[2 * i + 1] = w[i] & 0xFFFF0000u;
+                    }
+                    const BP p = FMT == MXFP4_ELEM_E4M3 ? block_params8(A) : block_params(A, a.mode, a.sf);
+                    e8 = p.e8;
+                    quant_block<FMT>(x, p, code);
+                }
+            } else {
+                uint32_t A = 0;
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    A = max(A, w[i] & 0x7FFFFFFFu);
+                const BP p = FMT == MXFP4_ELEM_E4M3 ? block_params8(A) : block_params(A, a.mode, a.sf);
+                e8 = p.e8;
+                quant_block<FMT>(w, p, code);
+            }
+        }
+        uint32_t word = e8 << (8 * (b & 3));
+        word |= __shfl_xor_sync(quad, word, 1);
+        word |= __shfl_xor_sync(quad, word, 2);
+        for (int j0 = 0; j0 < a.k; j0 += 8) {
+            uint32_t r[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                r[j] = j0 + j < a.k ? (uint32_t)rp[j0 + j] : 0xFFFFFFFFu;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (r[j] < a.out_rows) {
+                    if (b < nblk) {
+                        uint8_t* cp = a.codes + (int64_t)r[j] * a.code_ld + (int64_t)b * (4 * NC);
+                        if constexpr (NC == 8)
+                            st_cs_v8(cp, code);
+                        else
+                            st_stream(cp, make_uint4(code[0], code[1], code[2], code[3]));
+                    }
+                    if (a.ws_pair) {
+                        if (b == 0)
+                            a.ws_pair[r[j]] = (int32_t)(t * a.k) + j0 + j;
+                    } else if ((j & 3) == (int)(threadIdx.x & 3)) {
+                        *reinterpret_cast<uint32_t*>(a.scales + srow_off_mma(r[j], b & ~3u, nblk)) = word;
+                    }
+                }
+        }
+        if (a.ws_scales && (b & 3) == 0)
+            a.ws_scales[u >> 2] = word;
+        if (more) {
+#pragma unroll
+            for (int i = 0; i < NW; ++i)
+                w[i] = wn[i];
+        }
+    }
+    if (!a.ws_scales)
+        pad_scale_rows(a);
+}
+
+// The scale words of dispatch_stream_kernel's workspace into the atoms. Written
+// directly they are 4-byte stores, eight of which (of rows far apart in the
+// tokens' order) make a sector: 88 us for the whole dispatch of 8192 x 7168 to
+// 8 experts each, against 59.5 without the scales' stores. Here a CTA takes the
+// 128 rows of an atom row and SG_WORDS block columns of four, reads each row's
+// words as they lie in its token's, and writes whole atoms. A row's pair is
+// taken only if the pair's row is this one, so the list needs no initial state;
+// rows that no pair names stay as they were, rows behind out_rows are zeroed.
+constexpr int SG_WORDS = 32;
+
+__global__ void __launch_bounds__(NTHREADS) dispatch_scales_kernel(const DispatchArgs a)
+{
+    __shared__ uint32_t s_word[128][SG_WORDS + 1];
+    __shared__ int32_t s_token[128];   // a row's token; -1: no pair names the row, -2: behind the last row
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t ncb = ((a.cols + 31) / 32 + 3) / 4, pairs = a.tokens * a.k;
+    const int64_t row0 = (int64_t)blockIdx.x * 128, c0 = (int64_t)blockIdx.y * SG_WORDS;
+    if (threadIdx.x < 128) {
+        const int64_t r = row0 + threadIdx.x;
+        int32_t t = -2;
+        if (r < a.out_rows) {
+            const uint32_t p = (uint32_t)a.ws_pair[r];
+            t = p < pairs && a.rows[p] == r ? (int32_t)(p / (uint32_t)a.k) : -1;
+        }
+        s_token[threadIdx.x] = t;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int32_t t = s_token[16 * warp + i];
+        s_word[16 * warp + i][lane] = t >= 0 && c0 + lane < ncb ? a.ws_scales[(int64_t)t * ncb + c0 + lane] : 0u;
+    }
+    __syncthreads();
+    // word q of an atom is row 32 (q % 4) + q / 4
+    const int q = threadIdx.x & 127, i = 32 * (q & 3) + (q >> 2);
+    if (s_token[i] != -1)
+        for (int c = threadIdx.x >> 7; c < SG_WORDS && c0 + c < ncb; c += NTHREADS / 128)
+            reinterpret_cast<uint32_t*>(a.scales)[((int64_t)blockIdx.x * ncb + c0 + c) * 128 + q] = s_word[i][c];
+}
 
 struct CombineArgs {
     const void* y;          // [y_rows][ld_y]
@@ -201,16 +402,27 @@ __global__ void __launch_bounds__(NTHREADS) combine_kernel(const CombineArgs a)
 #pragma unroll
         for (int i = 0; i < N; ++i)
             acc[i] = 0.0f;
-        for (int j = 0; j < a.k; ++j) {
-            const uint32_t r = (uint32_t)a.rows[t * a.k + j];
-            if (r >= a.y_rows)
-                continue;
-            const float w = a.weights ? a.weights[t * a.k + j] : 1.0f;
-            float v[N];
-            piece_load<ESZ, N>(a.y, (int64_t)r * a.ld_y + c, v);
+        // four rows' loads in flight at a time
+        for (int j0 = 0; j0 < a.k; j0 += 4) {
+            float v[4][N], w[4];
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-                acc[i] = fmaf(w, v[i], acc[i]);
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t r = j0 + j < a.k ? (uint32_t)a.rows[t * a.k + j0 + j] : 0xFFFFFFFFu;
+                const bool some = r < a.y_rows;
+                w[j] = some ? (a.weights ? a.weights[t * a.k + j0 + j] : 1.0f) : 0.0f;
+                if (some) {
+                    piece_load<ESZ, N>(a.y, (int64_t)r * a.ld_y + c, v[j]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < N; ++i)
+                        v[j][i] = 0.0f;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+                    acc[i] = fmaf(w[j], v[j][i], acc[i]);
         }
         if (a.residual) {
             float v[N];
@@ -223,11 +435,15 @@ __global__ void __launch_bounds__(NTHREADS) combine_kernel(const CombineArgs a)
     }
 }
 
+// grad_y[rows[t][j]] = w[t][j] grad[t], grad_w[t][j] = grad[t] . y[rows[t][j]].
+// One CTA per token, which goes through its rows one by one (its gradient is
+// read again from the caches for each). Bound by memory; what counts is many
+// resident warps: holding the gradient and the next row in registers (two CTAs
+// per SM instead of six) took 117 us where this takes 80, a warp per row 143
+// (4099 tokens of 6 x 4096, bf16). The dot products are summed per thread, over
+// the lanes and over the warps, in order.
 constexpr int CB_MAX_K = 32;
 
-// grad_y[rows[t][j]] = w[t][j] grad[t], grad_w[t][j] = grad[t] . y[rows[t][j]].
-// One CTA per token; the dot products are summed per thread, then over the
-// warps' lanes and the warps, in a fixed order.
 template <int ESZ, bool VEC>
 __global__ void __launch_bounds__(NTHREADS) combine_bwd_kernel(const CombineArgs a)
 {
@@ -238,10 +454,9 @@ __global__ void __launch_bounds__(NTHREADS) combine_bwd_kernel(const CombineArgs
     const int64_t pieces = a.cols / N;
     for (int j = 0; j < a.k; ++j) {
         const uint32_t r = (uint32_t)a.rows[t * a.k + j];
-        const bool some = r < a.y_rows;
         const float w = a.weights ? a.weights[t * a.k + j] : 1.0f;
         float dot = 0.0f;
-        if (some)
+        if (r < a.y_rows)
             for (int64_t p = tid; p < pieces; p += NTHREADS) {
                 float g[N], v[N];
                 piece_load<ESZ, N>(a.grad, t * a.ld_out + p * N, g);
@@ -265,6 +480,7 @@ __global__ void __launch_bounds__(NTHREADS) combine_bwd_kernel(const CombineArgs
     __syncthreads();
     if (a.grad_w && tid < a.k) {
         float v = 0.0f;
+#pragma unroll
         for (int w = 0; w < NTHREADS / 32; ++w)
             v += s_dot[tid][w];
         a.grad_w[t * a.k + tid] = v;

@@ -318,6 +318,45 @@ def test_dispatch_every_bf16_value():
         assert np.array_equal(r.codes.cpu().numpy(), q["codes"])
 
 
+@pytest.mark.parametrize("fmt,dtype", [("e2m1", "bf16"), ("e4m3", "fp32")])
+@pytest.mark.parametrize("masked", [0.0, 0.3])
+def test_dispatch_of_many_rows(fmt, dtype, masked):
+    """Large enough for the scales' second kernel; odd row and block counts, rows left out."""
+    tokens, k, cols = 1400, 8, 6176          # 193 blocks: the last atom column holds one
+    rows, slots, _ = a_plan(tokens, 20, k, seed=3, masked=masked)
+    x = rnd(tokens, cols, seed=2, std=3.0, dtype=DT[dtype])
+    n = tokens * k + 5
+    assert ops._abi.lib().mxfp4_moe_dispatch_workspace(tokens, k, cols, n) > 0
+    width = cols if fmt == "e4m3" else cols // 2
+    codes = torch.full((n, width), 0xA5, dtype=torch.uint8, device="cuda")
+    scales = torch.full((ops.scales_row_bytes(n, cols, 32, "mma"),), 0x5A, dtype=torch.uint8, device="cuda")
+    ops.mxfp4_moe_dispatch(x.cuda(), rows.cuda(), elem_format=fmt, scale_mode="floor", row_count=n, out=ops.DispatchResult(codes=codes, scales=scales))
+    q = ops.mxfp4_qdq_fwd(x.cuda(), emit_values=False, emit_codes=True, elem_format=fmt, scale_mode="floor")   # checked against the oracle elsewhere
+    total = int((slots >= 0).sum())
+    token = (slots[:total].long() // k).cuda()
+    assert torch.equal(codes[:total], q.codes_row[token]) and bool((codes[total:] == 0xA5).all())
+    nblk = cols // 32
+    full = np.full((-(-n // 128) * 128, -(-nblk // 4) * 4), 0x5A, np.uint8)
+    full[n:] = 0
+    full[:total, :nblk] = q.scales_row[token].cpu().numpy()
+    full[:total, nblk:] = 0
+    assert np.array_equal(scales.cpu().numpy(), O.mma_scale_layout(full).reshape(-1))
+
+
+def test_dispatch_fp32_values_beside_the_ties():
+    """fp32 values one step below, at and above every midpoint and code, both signs, at several scales."""
+    base = torch.tensor([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+    near = torch.cat([base, torch.nextafter(base, torch.tensor(0.0)), torch.nextafter(base, torch.tensor(9.0))])
+    v = torch.cat([near, -near])
+    x = torch.stack([torch.cat([v[i:i + 31].roll(0), torch.tensor([6.0])]) if i + 31 <= v.numel() else torch.cat([v[-31:], torch.tensor([6.0])])
+                     for i in range(0, v.numel(), 31)])
+    x = torch.cat([x * 2.0 ** e for e in (-120, -60, -3, 0, 5, 100)])
+    rows = torch.arange(x.shape[0], dtype=torch.int32).view(-1, 1)
+    for mode, code in (("page", O.SCALE_PAGE), ("floor", O.SCALE_FLOOR)):
+        r = ops.mxfp4_moe_dispatch(x.cuda(), rows.cuda(), emit_values=False, emit_codes=True, scale_mode=mode)
+        assert np.array_equal(r.codes.cpu().numpy(), O.qdq_rowwise(x.numpy(), 32, 6.0, code)["codes"])
+
+
 def test_dispatch_skips_rows_outside_and_strides():
     x = rnd(10, 100, seed=4, dtype=torch.bfloat16).cuda()[:, 1:97]
     rows = torch.arange(20, dtype=torch.int32).view(10, 2)
@@ -567,7 +606,8 @@ def slope_bound(z, act):
 @pytest.mark.parametrize("sizes,m,n", [([1], 1, 2), ([40, 0, 70, 1, 200], 320, 264), ([130], 130, 1026), ([0, 0], 5, 64), ([500, 12], 512, 4096)])
 def test_linear_backward(act, dtype, sizes, m, n):
     """Against autograd of the activation in 64 bits; the bias sums add the
-    unrounded gradients (64 rows by 8 warps, 8 warps, then the units in order)."""
+    unrounded gradients: a thread's rows of a unit of 32, at most 8 rows side by
+    side, then the group's units, in order."""
     width = n // 2 if act == "swiglu" else n
     z = rnd(m, n, seed=1, std=2.0, dtype=DT[dtype])
     gy = rnd(m, width, seed=2, dtype=DT[dtype])
@@ -589,7 +629,7 @@ def test_linear_backward(act, dtype, sizes, m, n):
     first = 0
     for i, size in enumerate(sizes):
         part = want[first:first + size]
-        chain = 8 + 8 + size // 64 + 1
+        chain = 32 + 8 + size // 32 + 1
         close(gb[i], part.sum(0), e[first:first + size].sum(0) + chain * U32 * part.abs().sum(0), "grad_bias")
         first += size
     none = ops.mxfp4_grouped_linear_bwd(gy.cuda(), z.cuda(), gl, group_list_type=1, activation=act, bias_grad=False, out=torch.zeros_like(out))
@@ -611,8 +651,8 @@ def test_linear_backward_strided():
     one = ops.mxfp4_grouped_linear_bwd(g[:, 7:53], z[:, 3:95], activation="swiglu")
     two = ops.mxfp4_grouped_linear_bwd(g[:, 7:53].contiguous(), z[:, 3:95].contiguous(), activation="swiglu")
     assert torch.equal(one[0], two[0])
-    # other threads hold the columns, the sums' order is the same
-    assert torch.equal(one[1], two[1])
+    # the same 70 values a column, added in another order: each order is off by at most 69 roundings of the partial sums
+    assert bool(((one[1] - two[1]).abs() <= 2 * 69 * U32 * one[0].abs().sum(0)).all())
 
 
 # ------------------------------------------------------------------ as they are used together

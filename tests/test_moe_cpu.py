@@ -163,7 +163,7 @@ def test_workspace_sizes(abi):
     assert L.mxfp4_moe_route_workspace(64, 256) == 0
     assert L.mxfp4_moe_route_workspace(65, 256) == 2 * 256 * 4
     assert L.mxfp4_moe_route_workspace(-1, 4) == -1
-    assert L.mxfp4_grouped_linear_workspace(130, 10, 3) == (2 + 3) * 10 * 4
+    assert L.mxfp4_grouped_linear_workspace(130, 10, 3) == (4 + 3) * 10 * 4
     assert L.mxfp4_grouped_linear_workspace(130, 10, 0) == -1
 
 
