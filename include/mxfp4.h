@@ -442,8 +442,10 @@ mxfp4_status mxfp4_dual_level_qdq(const mxfp4_dual_level_args* args, mxfp4_strea
 /*
  * Routing. Per token with logits x_0 .. x_{E-1} (fp32 or bf16):
  *   score   s_e = softmax(x)_e or 1 / (1 + exp(-x_e))
- *   key     s_e + bias_e (bias NULL: s_e), evaluated in 64 bits; an expert is
- *           closed to the token when x_e is -inf or bias_e is not finite
+ *   key     s_e + bias_e (bias NULL: s_e), compared in 64 bits (with no bias,
+ *           or one value for all experts, by x_e itself, which orders alike);
+ *           an expert is closed to the token when x_e is -inf or bias_e is not
+ *           finite
  *   groups  with num_groups > 1 the experts form num_groups runs of E /
  *           num_groups; the topk_groups groups of greatest rank
  *           (group_score; ties: the lower group) stay open

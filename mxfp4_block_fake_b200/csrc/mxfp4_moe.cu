@@ -114,6 +114,12 @@ static mxfp4_status route_args(const mxfp4_moe_route_args* A, RouteArgs* r)
     return MXFP4_OK;
 }
 
+template <int NV>
+static const void* route_fn(bool bf16)
+{
+    return bf16 ? (const void*)route_kernel<NV, true> : (const void*)route_kernel<NV, false>;
+}
+
 static mxfp4_status run_route(const mxfp4_moe_route_args* A, cudaStream_t s)
 {
     RouteArgs r;
@@ -149,7 +155,16 @@ static mxfp4_status run_route(const mxfp4_moe_route_args* A, cudaStream_t s)
     r.top2 = A->group_score == MXFP4_GROUP_TOP2;
     r.chunks = (int32_t)route_chunks(A->tokens);
     const size_t smem = (size_t)RT_WARPS * r.experts * 8 + (size_t)r.experts * 8 + (size_t)RT_CHUNK * r.k * 2;
-    mxfp4_status e = launch1((const void*)route_kernel, r.chunks, RT_THREADS, smem, r, s);
+    int nv = 1;  // experts per lane
+    while (32 * nv < r.experts)
+        nv *= 2;
+    r.per = r.experts / r.groups;
+    r.per_magic = r.per == 1 ? 0u : (uint32_t)((0x100000000ull + r.per - 1) / r.per);
+    r.lanes = r.per % nv == 0 && ((r.per / nv) & (r.per / nv - 1)) == 0 ? r.per / nv : 0;
+    r.vec = r.experts % nv == 0 && aligned(A->logits, 16) && (A->ld * (int64_t)esz) % 16 == 0;
+    const void* fn = nv == 1 ? route_fn<1>(r.bf16) : nv == 2 ? route_fn<2>(r.bf16) : nv == 4 ? route_fn<4>(r.bf16)
+                     : nv == 8 ? route_fn<8>(r.bf16) : nv == 16 ? route_fn<16>(r.bf16) : route_fn<32>(r.bf16);
+    mxfp4_status e = launch1(fn, r.chunks, RT_THREADS, smem, r, s);
     if (e == MXFP4_OK && r.chunks > 1)
         e = launch1((const void*)route_scan_kernel, (r.experts + 31) / 32, 1024, 0, r, s);
     if (e == MXFP4_OK && r.chunks > 1)

@@ -3,7 +3,14 @@
 // mxfp4_moe.cu; the definition is in include/mxfp4.h, mxfp4_moe_route).
 //
 // Selection is decided by real numbers (the keys s_e + b_e), so it must not
-// depend on how an exponential happens to round: keys are held in 64 bits.
+// depend on how an exponential happens to round. A warp takes a token, a lane
+// NV consecutive experts; keys are formed in fp32 with the approximate
+// exponential, and every comparison the answer rests on (between neighbours in
+// the sorted choice, at its end, and between the last group kept and the first
+// dropped) is checked against the keys' error bound. A token with a comparison
+// inside the bound is selected again in 64 bits (rt_select64). Without a bias
+// (or with a constant one) the score is monotone in the logit, and logits are
+// compared as they are.
 //
 // The order of the (token, expert) pairs by expert is a counting sort without
 // atomics on counters: a CTA takes RT_CHUNK consecutive tokens and keeps, per
@@ -36,6 +43,10 @@ struct RouteArgs {
     int32_t experts, k, groups, topk_groups;
     int32_t top2, sigmoid, renorm, bf16;
     int32_t chunks;
+    int32_t per;          // experts of a group
+    uint32_t per_magic;   // ceil(2^32 / per): e / per is the high word of e * per_magic (e < 1024); 0: per is 1
+    int32_t lanes;        // lanes of a group where groups are whole lanes, a power of two; else 0
+    int32_t vec;          // rows are whole 16-byte vectors per lane
 };
 
 __device__ __forceinline__ float rt_logit(const RouteArgs& a, int64_t t, int e)
@@ -66,7 +77,8 @@ __device__ __forceinline__ double rt_neg_inf() { return __longlong_as_double(0xF
 
 // The chosen experts of token t in 64 bits: lane j < k returns the j-th (-1:
 // none). sk: the warp's scratch of a.experts doubles. m: the row's largest logit.
-__device__ __noinline__ int rt_select64(const RouteArgs& a, int64_t t, double* sk, float m)
+// exact: the logits' order is the keys' (scores are formed for group ranks only).
+__device__ __noinline__ int rt_select64(const RouteArgs& a, int64_t t, double* sk, float m, bool exact)
 {
     const int lane = threadIdx.x & 31, E = a.experts;
     const double NI = rt_neg_inf();
@@ -79,12 +91,14 @@ __device__ __noinline__ int rt_select64(const RouteArgs& a, int64_t t, double* s
         sum += p;
     }
     sum = warp_sum(sum);
+    const bool ranks = a.groups > 1 && a.top2;
     for (int e = lane; e < E; e += 32) {
-        double key = a.sigmoid ? sk[e] : sk[e] / sum;
-        bool open = rt_logit(a, t, e) > -INFINITY;
+        const float x = rt_logit(a, t, e);
+        double key = exact && !ranks ? (double)x : a.sigmoid ? sk[e] : sk[e] / sum;
+        bool open = x > -INFINITY;
         if (a.bias) {
             const float b = a.bias[e];
-            key += (double)b;
+            key += exact && !ranks ? 0.0 : (double)b;
             open = open && fabsf(b) < INFINITY;
         }
         sk[e] = open ? key : NI;
@@ -92,7 +106,7 @@ __device__ __noinline__ int rt_select64(const RouteArgs& a, int64_t t, double* s
     __syncwarp();
     if (a.groups > 1) {
         // lane g: the rank of group g (best key, or the best two added)
-        const int per = E / a.groups;
+        const int per = a.per;
         double best = NI, next = NI;
         if (lane < a.groups)
             for (int i = 0; i < per; ++i) {
@@ -113,6 +127,12 @@ __device__ __noinline__ int rt_select64(const RouteArgs& a, int64_t t, double* s
         if (lane < a.groups && before >= a.topk_groups)
             for (int i = 0; i < per; ++i)
                 sk[lane * per + i] = NI;
+        __syncwarp();
+    }
+    if (exact && ranks) {
+        for (int e = lane; e < E; e += 32)
+            if (sk[e] != NI)
+                sk[e] = (double)rt_logit(a, t, e);
         __syncwarp();
     }
     int mine = -1;
@@ -142,6 +162,235 @@ __device__ __noinline__ int rt_select64(const RouteArgs& a, int64_t t, double* s
         __syncwarp();
     }
     return mine;
+}
+
+// Order-preserving bits of a float (not NaN): greater floats, greater words.
+__device__ __forceinline__ uint32_t rt_order(float v)
+{
+    const uint32_t b = __float_as_uint(v);
+    return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+
+__device__ __forceinline__ float rt_unorder(uint32_t u)
+{
+    return __uint_as_float(u ^ (u >> 31 ? 0x80000000u : 0xFFFFFFFFu));
+}
+
+// The NV logits of this lane (experts lane * NV ..): -inf behind the last expert.
+template <int NV, bool BF16>
+__device__ __forceinline__ void rt_load(const RouteArgs& a, int64_t t, float (&x)[NV])
+{
+    const int e0 = (threadIdx.x & 31) * NV;
+    const int64_t i0 = t * a.ld + e0;
+    if constexpr (NV * (BF16 ? 2 : 4) >= 16) {
+        if (a.vec) {
+            constexpr int W = NV * (BF16 ? 2 : 4) / 16;
+#pragma unroll
+            for (int j = 0; j < W; ++j) {
+                uint4 q = make_uint4(0u, 0u, 0u, 0u);
+                if (e0 < a.experts)
+                    q = ld_stream(static_cast<const char*>(a.logits) + i0 * (BF16 ? 2 : 4) + 16 * j);
+                const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int i = 0; i < NV / W; ++i)
+                    x[NV / W * j + i] = BF16 ? __uint_as_float(i & 1 ? u[i / 2] & 0xFFFF0000u : u[i / 2] << 16) : __uint_as_float(u[i % 4]);
+            }
+            if (e0 >= a.experts)
+#pragma unroll
+                for (int i = 0; i < NV; ++i)
+                    x[i] = -INFINITY;
+            return;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        x[i] = e0 + i < a.experts ? (BF16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.logits)[i0 + i] << 16)
+                                          : static_cast<const float*>(a.logits)[i0 + i])
+                                  : -INFINITY;
+}
+
+// Descending order of a lane's NV words (Batcher's odd-even merge sort).
+template <int NV>
+__device__ __forceinline__ void rt_sort(uint32_t (&v)[NV])
+{
+#pragma unroll
+    for (int p = 1; p < NV; p *= 2)
+#pragma unroll
+        for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+            for (int j = k % p; j + k < NV; j += 2 * k)
+#pragma unroll
+                for (int i = 0; i < k; ++i)
+                    if (i + j + k < NV && (i + j) / (2 * p) == (i + j + k) / (2 * p)) {
+                        const uint32_t hi = max(v[i + j], v[i + j + k]), lo = min(v[i + j], v[i + j + k]);
+                        v[i + j] = hi;
+                        v[i + j + k] = lo;
+                    }
+}
+
+// Bound on a key's error against the real s + b. s: the approximate exponential
+// is off by 2^-22.5 + |x| 2^-23 relative (x its argument), the quotient by 2^-22,
+// a softmax sum of at most 32 terms per lane by 37 2^-24; the logistic function
+// passes on at most (1 - s) of its argument's part, and where |x| is large s is
+// small enough for the absolute term. The sum with the bias rounds by 2^-24.
+// slack: what the key lost to the lane's index in its low bits.
+__device__ __forceinline__ float rt_key_error(bool sigmoid, float s, float key, float slack)
+{
+    return s * (sigmoid ? 0x1p-19f : 0x1p-17f) + fabsf(key) * (0x1p-22f + slack) + 0x1p-25f;
+}
+
+// The chosen experts of token t (lane j < k: the j-th, -1: none). x: this lane's
+// logits, b: their biases (NaN: none, closed), m: the row's largest logit, exact:
+// keys are the logits themselves. s_key: the warp's scratch of a.experts doubles.
+// Each lane sorts its keys once, as order-preserving words whose low bits hold
+// the lane's index (the lower expert first); the k rounds then take the largest
+// head and shift one lane's list.
+template <int NV, bool BF16>
+__device__ __forceinline__ int rt_select(const RouteArgs& a, int64_t t, const float (&x)[NV], const float (&b)[NV], bool exact,
+                                         float m, double* s_key)
+{
+    const int lane = threadIdx.x & 31, K = a.k;
+    float key[NV];
+    float total = 1.0f;
+    bool unsure = false;
+    if (exact && !(a.groups > 1 && a.top2)) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            key[i] = b[i] == b[i] ? x[i] : -INFINITY;
+    } else {
+        if (a.sigmoid) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                key[i] = __fdividef(1.0f, 1.0f + __expf(-x[i]));
+        } else {
+            total = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                key[i] = __expf(x[i] - m);
+                total += key[i];
+            }
+            total = warp_sum(total);
+            const float r = __fdividef(1.0f, total);
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                key[i] *= r;
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            key[i] = x[i] > -INFINITY && b[i] == b[i] ? key[i] + b[i] : -INFINITY;
+    }
+    uint32_t kept = 0xFFFFFFFFu;  // bit g: group g stays
+    if (a.groups > 1) {
+        // lane g: the two best keys of group g
+        float best = -INFINITY, next = -INFINITY;
+        if (a.lanes > 0) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                next = fmaxf(next, fminf(best, key[i]));
+                best = fmaxf(best, key[i]);
+            }
+            for (int o = a.lanes >> 1; o; o >>= 1) {
+                const float ob = __shfl_xor_sync(FULL, best, o), on = __shfl_xor_sync(FULL, next, o);
+                next = fmaxf(fminf(best, ob), fmaxf(next, on));
+                best = fmaxf(best, ob);
+            }
+            best = __shfl_sync(FULL, best, (lane * a.lanes) & 31);
+            next = __shfl_sync(FULL, next, (lane * a.lanes) & 31);
+        } else {
+            float* s = reinterpret_cast<float*>(s_key);
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                if (lane * NV + i < a.experts)
+                    s[lane * NV + i] = key[i];
+            __syncwarp();
+            if (lane < a.groups)
+                for (int i = 0; i < a.per; ++i) {
+                    const float v = s[lane * a.per + i];
+                    next = fmaxf(next, fminf(best, v));
+                    best = fmaxf(best, v);
+                }
+            __syncwarp();
+        }
+        float rank = lane < a.groups ? best : -INFINITY;
+        if (a.top2 && next > -INFINITY)
+            rank += next;
+        int before = 0;
+        for (int g = 0; g < a.groups; ++g) {
+            const float r = __shfl_sync(FULL, rank, g);
+            before += r > rank || (r == rank && g < lane);
+        }
+        const bool keep = lane < a.groups && before < a.topk_groups;
+        kept = __ballot_sync(FULL, keep);
+        if (!exact || a.top2) {
+            // the least rank kept against the greatest dropped; the error of a
+            // key's score is bounded by a score of |key| + the largest bias
+            float bm = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                bm = fmaxf(bm, fabsf(b[i]));
+            bm = warp_max(bm);
+            const float low = -warp_max(keep ? -rank : -INFINITY), high = warp_max(keep ? -INFINITY : rank);
+            const float size = fmaxf(fabsf(low), fabsf(high));
+            const float err = 2.0f * (rt_key_error(a.sigmoid, fminf(size + 2.0f * bm, 2.0f), size + 2.0f * bm, 0.0f) + 0x1p-25f);
+            unsure = high > -INFINITY && low - high <= 2.0f * err;
+        }
+        if (exact)  // the scores were for the groups' ranks
+#pragma unroll
+            for (int i = 0; i < NV; ++i)
+                key[i] = b[i] == b[i] ? x[i] : -INFINITY;
+    }
+    uint32_t v[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+        const bool open = key[i] > -INFINITY && ((kept >> (a.per_magic ? __umulhi(lane * NV + i, a.per_magic) : (uint32_t)(lane * NV + i) & 31u)) & 1u);
+        v[i] = open ? (rt_order(key[i]) & ~(uint32_t)(NV - 1)) | (uint32_t)(NV - 1 - i) : 0u;
+    }
+    rt_sort<NV>(v);
+    uint32_t word = 0u;   // lane j: the j-th choice's word (lane K: the one behind the last)
+    int src = 0;          // and its lane
+    for (int j = 0; j <= K; ++j) {
+        // equal keys: the lowest lane holds the lowest expert
+        const uint32_t head = v[0] & ~(uint32_t)(NV - 1), top = __reduce_max_sync(FULL, head);
+        if (top == 0u)
+            break;
+        const int at = __ffs(__ballot_sync(FULL, head == top)) - 1;
+        const uint32_t taken = __shfl_sync(FULL, v[0], at);
+        if (lane == j) {
+            word = taken;
+            src = at;
+        }
+        if (lane == at) {
+#pragma unroll
+            for (int i = 0; i + 1 < NV; ++i)
+                v[i] = v[i + 1];
+            v[NV - 1] = 0u;
+        }
+    }
+    const int e = word ? src * NV + (NV - 1 - (int)(word & (NV - 1))) : -1;
+    // bf16 logits are whole in their words: nothing to check
+    if (!(exact && BF16)) {
+        const float xe = e >= 0 ? rt_logit(a, t, e) : -INFINITY;
+        const float be = e >= 0 && a.bias ? a.bias[e] : 0.0f;
+        const float ke = e >= 0 ? rt_unorder(word & ~(uint32_t)(NV - 1)) : -INFINITY;
+        const float xn = __shfl_down_sync(FULL, xe, 1), bn = __shfl_down_sync(FULL, be, 1), kn = __shfl_down_sync(FULL, ke, 1);
+        const int en = __shfl_down_sync(FULL, e, 1);
+        bool close;
+        if (exact) {
+            close = lane < K - 1 ? !(xe > xn || (xe == xn && e < en)) : ke == kn;
+        } else {
+            const float se = fminf(fabsf(ke - be) * 1.0001f, 1.0f), sn = fminf(fabsf(kn - bn) * 1.0001f, 1.0f);
+            const float slack = NV * 0x1p-23f;
+            close = ke - kn <= rt_key_error(a.sigmoid, se, ke, slack) + rt_key_error(a.sigmoid, sn, kn, slack);
+            if (lane < K - 1 && xe == xn && be == bn)
+                close = false;  // equal keys, the lower expert first
+        }
+        // a lane whose successor exists; the 32nd choice's is not at hand
+        unsure = unsure || (lane < K && e >= 0 && (K < 32 || lane < 31 ? en >= 0 && close : true));
+    }
+    if (__any_sync(FULL, unsure))
+        return rt_select64(a, t, s_key, m, exact);
+    return lane < K ? e : -1;
 }
 
 // Score of a chosen expert (fp32): softmax e^(x - m) / sum, or the logistic
@@ -208,7 +457,8 @@ __device__ int rt_scan(const int* s_cnt, int* s_off, int n)
 
 // One CTA per chunk. A single chunk (chunks == 1) finishes the order itself;
 // else `rows` receives ranks within the chunk and ws the chunk's counts.
-__global__ void __launch_bounds__(RT_THREADS) route_kernel(const RouteArgs a)
+template <int NV, bool BF16>
+__global__ void __launch_bounds__(RT_THREADS, NV <= 8 ? 4 : 1) route_kernel(const __grid_constant__ RouteArgs a)
 {
     extern __shared__ __align__(16) uint8_t rt_dyn[];
     const int E = a.experts, K = a.k;
@@ -221,17 +471,40 @@ __global__ void __launch_bounds__(RT_THREADS) route_kernel(const RouteArgs a)
     for (int i = tid; i < 2 * E; i += RT_THREADS)
         s_bits[i] = 0u;
     __syncthreads();
+    float x[NV], b[NV];
+    // biases: NaN closes an expert (a bias that is not finite does); one value
+    // for all open experts leaves the order to the logits
+    bool exact = true;
+    if (a.bias) {
+        float low = INFINITY, high = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            b[i] = lane * NV + i < E ? a.bias[lane * NV + i] : 0.0f;
+            if (!(fabsf(b[i]) < INFINITY))
+                b[i] = __uint_as_float(QNAN32);
+            else if (lane * NV + i < E) {
+                low = fminf(low, b[i]);
+                high = fmaxf(high, b[i]);
+            }
+        }
+        exact = -warp_max(-low) >= warp_max(high);
+    } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            b[i] = 0.0f;
+    }
     for (int i = warp; i < nt; i += RT_WARPS) {
         const int64_t t = t0 + i;
         int mine = -1;
         float w = 0.0f;
         if (!a.token_mask || a.token_mask[t]) {
+            rt_load<NV, BF16>(a, t, x);
             float m = -INFINITY;
             bool bad = false;
-            for (int e = lane; e < E; e += 32) {
-                const float x = rt_logit(a, t, e);
-                bad |= !(x < INFINITY);
-                m = fmaxf(m, x);
+#pragma unroll
+            for (int e = 0; e < NV; ++e) {
+                bad |= !(x[e] < INFINITY);
+                m = fmaxf(m, x[e]);
             }
             m = warp_max(m);
             if (__any_sync(FULL, bad)) {
@@ -240,11 +513,12 @@ __global__ void __launch_bounds__(RT_THREADS) route_kernel(const RouteArgs a)
             } else if (m > -INFINITY) {
                 float sum = 0.0f;
                 if (!a.sigmoid && !a.renorm) {
-                    for (int e = lane; e < E; e += 32)
-                        sum += expf(rt_logit(a, t, e) - m);
+#pragma unroll
+                    for (int e = 0; e < NV; ++e)
+                        sum += expf(x[e] - m);
                     sum = warp_sum(sum);
                 }
-                mine = rt_select64(a, t, s_key, m);
+                mine = rt_select<NV, BF16>(a, t, x, b, exact, m, s_key);
                 w = rt_weight(a, t, mine, m, sum);
             }
         }

@@ -132,6 +132,33 @@ def test_route_near_ties_are_decided_in_64_bits():
     check_route(x, k, score="softmax", bias=(0.6 - torch.softmax(base, 0) + 1e-9 * order.double()).float(), num_groups=4, topk_groups=2)
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("bias_kind", ["none", "zero", "small", "some"])
+@pytest.mark.parametrize("experts,groups,topk_groups,k", [(256, 1, 1, 8), (256, 8, 4, 8), (60, 4, 3, 6), (1000, 10, 4, 12), (512, 32, 5, 9), (64, 1, 1, 32)])
+def test_route_choice_of_many_tokens(dtype, score, bias_kind, experts, groups, topk_groups, k):
+    """The choice against 64-bit keys sorted stably, over enough tokens that
+    neighbouring keys come close to one another (and, in bf16, coincide)."""
+    t = 6000
+    x = rnd(t, experts, seed=21, std=1.0, dtype=DT[dtype]).cuda()
+    bias = {"none": None, "zero": torch.zeros(experts), "small": rnd(experts, seed=22, std=1e-3),
+            "some": (torch.arange(experts) % 3 == 0).float() * 0.01}[bias_kind]
+    v = x.double()
+    key = torch.sigmoid(v) if score == "sigmoid" else torch.softmax(v, 1)
+    if bias is not None:
+        bias = bias.cuda()
+        key = key + bias.double()
+    if groups > 1:
+        by = key.view(t, groups, -1)
+        rank = by.topk(2, 2).values.sum(2)
+        keep = torch.zeros(t, groups, dtype=torch.bool, device="cuda").scatter_(1, rank.sort(dim=1, descending=True, stable=True).indices[:, :topk_groups], True)
+        key = torch.where(keep[:, :, None], by, -torch.inf).view(t, experts)
+    want = key.sort(dim=1, descending=True, stable=True).indices[:, :k]
+    r = ops.mxfp4_moe_route(x, k, score=score, bias=bias, num_groups=groups, topk_groups=topk_groups)
+    # softmax in 64 bits may round two different logits' keys to one only where they are 2^-52 apart: none here
+    assert torch.equal(r.experts.long(), want)
+
+
 @pytest.mark.parametrize("tokens", [0, 1, 64, 65, 2048, 2049, 5000])
 def test_route_order_of_many_tokens(tokens):
     """The expert-sorted order against a stable sort (experts from the call)."""
