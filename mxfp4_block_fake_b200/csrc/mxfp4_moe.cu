@@ -115,9 +115,11 @@ static mxfp4_status route_args(const mxfp4_moe_route_args* A, RouteArgs* r)
 }
 
 template <int NV>
-static const void* route_fn(bool bf16)
+static const void* route_fn(bool bf16, bool sigmoid)
 {
-    return bf16 ? (const void*)route_kernel<NV, true> : (const void*)route_kernel<NV, false>;
+    if (sigmoid)
+        return bf16 ? (const void*)route_kernel<NV, true, true> : (const void*)route_kernel<NV, false, true>;
+    return bf16 ? (const void*)route_kernel<NV, true, false> : (const void*)route_kernel<NV, false, false>;
 }
 
 static mxfp4_status run_route(const mxfp4_moe_route_args* A, cudaStream_t s)
@@ -162,8 +164,9 @@ static mxfp4_status run_route(const mxfp4_moe_route_args* A, cudaStream_t s)
     r.per_magic = r.per == 1 ? 0u : (uint32_t)((0x100000000ull + r.per - 1) / r.per);
     r.lanes = r.per % nv == 0 && ((r.per / nv) & (r.per / nv - 1)) == 0 ? r.per / nv : 0;
     r.vec = r.experts % nv == 0 && aligned(A->logits, 16) && (A->ld * (int64_t)esz) % 16 == 0;
-    const void* fn = nv == 1 ? route_fn<1>(r.bf16) : nv == 2 ? route_fn<2>(r.bf16) : nv == 4 ? route_fn<4>(r.bf16)
-                     : nv == 8 ? route_fn<8>(r.bf16) : nv == 16 ? route_fn<16>(r.bf16) : route_fn<32>(r.bf16);
+    const bool b = r.bf16, g = r.sigmoid;
+    const void* fn = nv == 1 ? route_fn<1>(b, g) : nv == 2 ? route_fn<2>(b, g) : nv == 4 ? route_fn<4>(b, g)
+                     : nv == 8 ? route_fn<8>(b, g) : nv == 16 ? route_fn<16>(b, g) : route_fn<32>(b, g);
     mxfp4_status e = launch1(fn, r.chunks, RT_THREADS, smem, r, s);
     if (e == MXFP4_OK && r.chunks > 1)
         e = launch1((const void*)route_scan_kernel, (r.experts + 31) / 32, 1024, 0, r, s);

@@ -49,6 +49,14 @@ struct RouteArgs {
     int32_t vec;          // rows are whole 16-byte vectors per lane
 };
 
+template <bool BF16>
+__device__ __forceinline__ float rt_logit(const RouteArgs& a, int64_t t, int e)
+{
+    const int64_t i = t * a.ld + e;
+    return BF16 ? __uint_as_float((uint32_t)static_cast<const uint16_t*>(a.logits)[i] << 16)
+                : static_cast<const float*>(a.logits)[i];
+}
+
 __device__ __forceinline__ float rt_logit(const RouteArgs& a, int64_t t, int e)
 {
     const int64_t i = t * a.ld + e;
@@ -56,12 +64,26 @@ __device__ __forceinline__ float rt_logit(const RouteArgs& a, int64_t t, int e)
                   : static_cast<const float*>(a.logits)[i];
 }
 
+// The warp's greatest value; NaN if any is NaN.
 __device__ __forceinline__ float warp_max(float v)
 {
-#pragma unroll
-    for (int o = 16; o; o >>= 1)
-        v = fmaxf(v, __shfl_xor_sync(FULL, v, o));
-    return v;
+    float r;
+    asm volatile("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+__device__ __forceinline__ float rcp_approx(float v)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
 }
 
 template <typename T>
@@ -228,56 +250,65 @@ __device__ __forceinline__ void rt_sort(uint32_t (&v)[NV])
                     }
 }
 
-// Bound on a key's error against the real s + b. s: the approximate exponential
-// is off by 2^-22.5 + |x| 2^-23 relative (x its argument), the quotient by 2^-22,
-// a softmax sum of at most 32 terms per lane by 37 2^-24; the logistic function
-// passes on at most (1 - s) of its argument's part, and where |x| is large s is
-// small enough for the absolute term. The sum with the bias rounds by 2^-24.
-// slack: what the key lost to the lane's index in its low bits.
-__device__ __forceinline__ float rt_key_error(bool sigmoid, float s, float key, float slack)
+__device__ __forceinline__ float exp2_approx(float v)
 {
-    return s * (sigmoid ? 0x1p-19f : 0x1p-17f) + fabsf(key) * (0x1p-22f + slack) + 0x1p-25f;
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// Approximate score of a logit: the logistic function, or e^(x - m) times r.
+template <bool SIG>
+__device__ __forceinline__ float rt_score(float x, float m, float r)
+{
+    if constexpr (SIG)
+        return rcp_approx(1.0f + exp2_approx(-1.4426950408889634f * x));
+    else
+        return exp2_approx(1.4426950408889634f * (x - m)) * r;
+}
+
+// Bound on a key's error against the real s + b. The approximate exponential is
+// off by 2^-22.5 + |x| 2^-23 relative (x its argument: 2^-19 up to 14; beyond,
+// the value itself is below 2^-20 and the absolute term covers it), of which
+// the logistic function passes on 1 - s; its sum and reciprocal, and a softmax
+// sum of at most 32 terms per lane, its reciprocal and product add less than
+// 2^-21.5 and 2^-18; the sum with the bias rounds by 2^-24 of the key.
+template <bool SIG>
+__device__ __forceinline__ float rt_key_error(float s, float key)
+{
+    return s * (SIG ? fmaf(1.0f - s, 0x1p-19f, 0x1p-21f) : 0x1p-17f) + fabsf(key) * 0x1p-23f + 0x1p-25f;
 }
 
 // The chosen experts of token t (lane j < k: the j-th, -1: none). x: this lane's
-// logits, b: their biases (NaN: none, closed), m: the row's largest logit, exact:
-// keys are the logits themselves. s_key: the warp's scratch of a.experts doubles.
-// Each lane sorts its keys once, as order-preserving words whose low bits hold
-// the lane's index (the lower expert first); the k rounds then take the largest
-// head and shift one lane's list.
-template <int NV, bool BF16>
-__device__ __forceinline__ int rt_select(const RouteArgs& a, int64_t t, const float (&x)[NV], const float (&b)[NV], bool exact,
-                                         float m, double* s_key)
+// logits, b: their biases (-inf: closed), bm: the largest |bias|, m: the row's
+// largest logit, exact: the logits' order is the keys'. s_key: the warp's
+// scratch of a.experts doubles; xe receives the choice's logit. Each lane sorts its keys once, as
+// order-preserving words whose low bits hold the lane's index (the lower expert
+// first); the k rounds then take the largest head and shift one lane's list.
+template <int NV, bool BF16, bool SIG>
+__device__ __forceinline__ int rt_select(const RouteArgs& a, int64_t t, const float (&x)[NV], const float (&b)[NV], float bm,
+                                         bool exact, float m, double* s_key, float& xe)
 {
     const int lane = threadIdx.x & 31, K = a.k;
-    float key[NV];
-    float total = 1.0f;
+    constexpr uint32_t INDEX = NV - 1;
+    float key[NV], r = 1.0f;
     bool unsure = false;
     if (exact && !(a.groups > 1 && a.top2)) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            key[i] = b[i] == b[i] ? x[i] : -INFINITY;
+            key[i] = b[i] > -INFINITY ? x[i] : -INFINITY;
     } else {
-        if (a.sigmoid) {
+        if constexpr (!SIG) {
+            float total = 0.0f;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                key[i] = __fdividef(1.0f, 1.0f + __expf(-x[i]));
-        } else {
-            total = 0.0f;
-#pragma unroll
-            for (int i = 0; i < NV; ++i) {
-                key[i] = __expf(x[i] - m);
-                total += key[i];
-            }
-            total = warp_sum(total);
-            const float r = __fdividef(1.0f, total);
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                key[i] *= r;
+                total += rt_score<false>(x[i], m, 1.0f);
+            r = rcp_approx(warp_sum(total));
         }
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-            key[i] = x[i] > -INFINITY && b[i] == b[i] ? key[i] + b[i] : -INFINITY;
+        for (int i = 0; i < NV; ++i) {
+            key[i] = x[i] > -INFINITY ? rt_score<SIG>(x[i], m, r) + b[i] : -INFINITY;
+        }
     }
     uint32_t kept = 0xFFFFFFFFu;  // bit g: group g stays
     if (a.groups > 1) {
@@ -315,44 +346,58 @@ __device__ __forceinline__ int rt_select(const RouteArgs& a, int64_t t, const fl
         float rank = lane < a.groups ? best : -INFINITY;
         if (a.top2 && next > -INFINITY)
             rank += next;
-        int before = 0;
-        for (int g = 0; g < a.groups; ++g) {
-            const float r = __shfl_sync(FULL, rank, g);
-            before += r > rank || (r == rank && g < lane);
+        int before = 0;  // groups ahead of this lane's (lane g: group g)
+        if (a.groups <= 8) {
+            // lane (g, quarter): two comparisons of the eight of group g
+            const int g = lane & 7, h = (lane >> 3) * 2;
+            const float mine = __shfl_sync(FULL, rank, g), r0 = __shfl_sync(FULL, rank, h), r1 = __shfl_sync(FULL, rank, h + 1);
+            before = (int)(r0 > mine || (r0 == mine && h < g)) + (int)(r1 > mine || (r1 == mine && h + 1 < g));
+            before += __shfl_xor_sync(FULL, before, 8);
+            before += __shfl_xor_sync(FULL, before, 16);
+        } else {
+#pragma unroll 4
+            for (int g = 0; g < a.groups; ++g) {
+                const float rg = __shfl_sync(FULL, rank, g);
+                before += rg > rank || (rg == rank && g < lane);
+            }
         }
         const bool keep = lane < a.groups && before < a.topk_groups;
         kept = __ballot_sync(FULL, keep);
         if (!exact || a.top2) {
-            // the least rank kept against the greatest dropped; the error of a
-            // key's score is bounded by a score of |key| + the largest bias
-            float bm = 0.0f;
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-                bm = fmaxf(bm, fabsf(b[i]));
-            bm = warp_max(bm);
+            // the least rank kept against the greatest dropped: a rank is one or
+            // two keys, whose scores are at most 1 and sum to |rank| + 2 bm
             const float low = -warp_max(keep ? -rank : -INFINITY), high = warp_max(keep ? -INFINITY : rank);
-            const float size = fmaxf(fabsf(low), fabsf(high));
-            const float err = 2.0f * (rt_key_error(a.sigmoid, fminf(size + 2.0f * bm, 2.0f), size + 2.0f * bm, 0.0f) + 0x1p-25f);
+            const float size = fmaxf(fabsf(low), fabsf(high)) + 2.0f * bm;
+            const float err = fminf(size, 2.0f) * (SIG ? 0x1p-19f : 0x1p-17f) + size * 0x1p-22f + 0x1p-24f;
             unsure = high > -INFINITY && low - high <= 2.0f * err;
         }
         if (exact)  // the scores were for the groups' ranks
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                key[i] = b[i] == b[i] ? x[i] : -INFINITY;
+                key[i] = b[i] > -INFINITY ? x[i] : -INFINITY;
     }
+    // words at or below that of -inf are closed
+    constexpr uint32_t CLOSED = 0x007FFFFFu;
     uint32_t v[NV];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const bool open = key[i] > -INFINITY && ((kept >> (a.per_magic ? __umulhi(lane * NV + i, a.per_magic) : (uint32_t)(lane * NV + i) & 31u)) & 1u);
-        v[i] = open ? (rt_order(key[i]) & ~(uint32_t)(NV - 1)) | (uint32_t)(NV - 1 - i) : 0u;
+    for (int i = 0; i < NV; ++i)
+        v[i] = (rt_order(key[i]) & ~INDEX) | (INDEX - i);
+    if (a.groups > 1 && a.lanes == 0) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const uint32_t e = lane * NV + i;
+            v[i] = (kept >> (a.per_magic ? __umulhi(e, a.per_magic) : e & 31u)) & 1u ? v[i] : 0u;
+        }
     }
     rt_sort<NV>(v);
+    if (a.groups > 1 && a.lanes > 0 && !((kept >> (lane / a.lanes)) & 1u))
+        v[0] = 0u;  // a lane of one group that was dropped: its list is never entered
     uint32_t word = 0u;   // lane j: the j-th choice's word (lane K: the one behind the last)
     int src = 0;          // and its lane
     for (int j = 0; j <= K; ++j) {
         // equal keys: the lowest lane holds the lowest expert
-        const uint32_t head = v[0] & ~(uint32_t)(NV - 1), top = __reduce_max_sync(FULL, head);
-        if (top == 0u)
+        const uint32_t head = v[0] & ~INDEX, top = __reduce_max_sync(FULL, head);
+        if (top <= CLOSED)
             break;
         const int at = __ffs(__ballot_sync(FULL, head == top)) - 1;
         const uint32_t taken = __shfl_sync(FULL, v[0], at);
@@ -367,43 +412,60 @@ __device__ __forceinline__ int rt_select(const RouteArgs& a, int64_t t, const fl
             v[NV - 1] = 0u;
         }
     }
-    const int e = word ? src * NV + (NV - 1 - (int)(word & (NV - 1))) : -1;
+    const int e = word ? src * NV + (int)(INDEX - (word & INDEX)) : -1;
     // bf16 logits are whole in their words: nothing to check
+    xe = e >= 0 ? rt_logit<BF16>(a, t, e) : -INFINITY;
     if (!(exact && BF16)) {
-        const float xe = e >= 0 ? rt_logit(a, t, e) : -INFINITY;
         const float be = e >= 0 && a.bias ? a.bias[e] : 0.0f;
-        const float ke = e >= 0 ? rt_unorder(word & ~(uint32_t)(NV - 1)) : -INFINITY;
-        const float xn = __shfl_down_sync(FULL, xe, 1), bn = __shfl_down_sync(FULL, be, 1), kn = __shfl_down_sync(FULL, ke, 1);
+        const float xn = __shfl_down_sync(FULL, xe, 1), bn = __shfl_down_sync(FULL, be, 1);
         const int en = __shfl_down_sync(FULL, e, 1);
+        const uint32_t wn = __shfl_down_sync(FULL, word, 1);
         bool close;
         if (exact) {
-            close = lane < K - 1 ? !(xe > xn || (xe == xn && e < en)) : ke == kn;
+            close = lane < K - 1 ? !(xe > xn || (xe == xn && e < en)) : ((word ^ wn) & ~INDEX) == 0u;
         } else {
-            const float se = fminf(fabsf(ke - be) * 1.0001f, 1.0f), sn = fminf(fabsf(kn - bn) * 1.0001f, 1.0f);
-            const float slack = NV * 0x1p-23f;
-            close = ke - kn <= rt_key_error(a.sigmoid, se, ke, slack) + rt_key_error(a.sigmoid, sn, kn, slack);
+            // the whole keys again; behind the last choice nothing exceeds the
+            // next word with its low bits full
+            const float se = rt_score<SIG>(xe, m, r), sn = rt_score<SIG>(xn, m, r), ke = se + be, kn = sn + bn;
+            const float bound = lane < K - 1 ? kn : rt_unorder(wn | INDEX);
+            close = ke - bound <= rt_key_error<SIG>(se, ke) + rt_key_error<SIG>(sn, kn);
             if (lane < K - 1 && xe == xn && be == bn)
-                close = false;  // equal keys, the lower expert first
+                close = e > en;  // equal keys: the lower expert first
         }
         // a lane whose successor exists; the 32nd choice's is not at hand
         unsure = unsure || (lane < K && e >= 0 && (K < 32 || lane < 31 ? en >= 0 && close : true));
     }
-    if (__any_sync(FULL, unsure))
-        return rt_select64(a, t, s_key, m, exact);
-    return lane < K ? e : -1;
+    int mine = lane < K ? e : -1;
+    if (__any_sync(FULL, unsure)) {
+        mine = rt_select64(a, t, s_key, m, exact);
+        xe = mine >= 0 ? rt_logit<BF16>(a, t, mine) : -INFINITY;
+    }
+    if (mine < 0)
+        xe = -INFINITY;
+    return mine;
 }
 
 // Score of a chosen expert (fp32): softmax e^(x - m) / sum, or the logistic
 // function. With renormalisation a common factor cancels, so scores that
 // underflow are taken relative to the chosen ones' largest logit.
-__device__ __forceinline__ float rt_sigmoid(float x)
+__device__ __forceinline__ float rt_sigmoid(float x) { return __fdividef(1.0f, 1.0f + expf(-x)); }
+
+// Sum over the k slots' lanes (0 in the others).
+__device__ __forceinline__ float rt_sum_k(const RouteArgs& a, float v)
 {
-    return x >= 0.0f ? 1.0f / (1.0f + expf(-x)) : expf(x) / (1.0f + expf(x));
+    if (a.k > 8) {
+        v += __shfl_xor_sync(FULL, v, 16);
+        v += __shfl_xor_sync(FULL, v, 8);
+    }
+#pragma unroll
+    for (int o = 4; o; o >>= 1)
+        v += __shfl_xor_sync(FULL, v, o);
+    return v;
 }
 
-__device__ __forceinline__ float rt_weight(const RouteArgs& a, int64_t t, int mine, float m, float sum)
+// x: the choice's logit, -inf where there is none.
+__device__ __forceinline__ float rt_weight(const RouteArgs& a, int mine, float x, float m, float sum)
 {
-    const float x = mine >= 0 ? rt_logit(a, t, mine) : -INFINITY;
     float s;
     if (a.renorm) {
         const float top = warp_max(x);
@@ -414,8 +476,8 @@ __device__ __forceinline__ float rt_weight(const RouteArgs& a, int64_t t, int mi
             s = expf(x - top);
         }
         s = mine >= 0 ? s : 0.0f;
-        const float total = warp_sum(s);
-        return total > 0.0f ? a.scale * (s / total) : 0.0f;
+        const float total = rt_sum_k(a, s);
+        return total > 0.0f ? a.scale * __fdividef(s, total) : 0.0f;
     }
     s = a.sigmoid ? rt_sigmoid(x) : expf(x - m) / sum;
     return mine >= 0 ? a.scale * s : 0.0f;
@@ -457,7 +519,7 @@ __device__ int rt_scan(const int* s_cnt, int* s_off, int n)
 
 // One CTA per chunk. A single chunk (chunks == 1) finishes the order itself;
 // else `rows` receives ranks within the chunk and ws the chunk's counts.
-template <int NV, bool BF16>
+template <int NV, bool BF16, bool SIG>
 __global__ void __launch_bounds__(RT_THREADS, NV <= 8 ? 4 : 1) route_kernel(const __grid_constant__ RouteArgs a)
 {
     extern __shared__ __align__(16) uint8_t rt_dyn[];
@@ -472,22 +534,26 @@ __global__ void __launch_bounds__(RT_THREADS, NV <= 8 ? 4 : 1) route_kernel(cons
         s_bits[i] = 0u;
     __syncthreads();
     float x[NV], b[NV];
-    // biases: NaN closes an expert (a bias that is not finite does); one value
-    // for all open experts leaves the order to the logits
+    // biases: one that is not finite closes its expert (-inf does in the keys);
+    // one value for all open experts leaves the order to the logits
     bool exact = true;
+    float bm = 0.0f;
     if (a.bias) {
         float low = INFINITY, high = -INFINITY;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             b[i] = lane * NV + i < E ? a.bias[lane * NV + i] : 0.0f;
             if (!(fabsf(b[i]) < INFINITY))
-                b[i] = __uint_as_float(QNAN32);
+                b[i] = -INFINITY;
             else if (lane * NV + i < E) {
                 low = fminf(low, b[i]);
                 high = fmaxf(high, b[i]);
             }
         }
-        exact = -warp_max(-low) >= warp_max(high);
+        low = -warp_max(-low);
+        high = warp_max(high);
+        exact = low >= high;
+        bm = fmaxf(fabsf(low), fabsf(high));  // infinite where no expert is open: then no key is compared
     } else {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
@@ -499,27 +565,25 @@ __global__ void __launch_bounds__(RT_THREADS, NV <= 8 ? 4 : 1) route_kernel(cons
         float w = 0.0f;
         if (!a.token_mask || a.token_mask[t]) {
             rt_load<NV, BF16>(a, t, x);
-            float m = -INFINITY;
-            bool bad = false;
+            float m = x[0];
 #pragma unroll
-            for (int e = 0; e < NV; ++e) {
-                bad |= !(x[e] < INFINITY);
-                m = fmaxf(m, x[e]);
-            }
+            for (int e = 1; e < NV; ++e)
+                m = max_nan(m, x[e]);
             m = warp_max(m);
-            if (__any_sync(FULL, bad)) {
+            if (!(m < INFINITY)) {  // a NaN or +inf
                 mine = lane < K ? lane : -1;
                 w = __uint_as_float(QNAN32);
             } else if (m > -INFINITY) {
                 float sum = 0.0f;
-                if (!a.sigmoid && !a.renorm) {
+                if (!SIG && !a.renorm) {
 #pragma unroll
                     for (int e = 0; e < NV; ++e)
                         sum += expf(x[e] - m);
                     sum = warp_sum(sum);
                 }
-                mine = rt_select<NV, BF16>(a, t, x, b, exact, m, s_key);
-                w = rt_weight(a, t, mine, m, sum);
+                float xe;
+                mine = rt_select<NV, BF16, SIG>(a, t, x, b, bm, exact, m, s_key, xe);
+                w = rt_weight(a, mine, xe, m, sum);
             }
         }
         if (lane < K) {
