@@ -167,16 +167,34 @@ __device__ int64_t ln_plan(const Args& a, int32_t* s_tpre, int32_t* s_rst)
 // 2^-23 plus |z| 2^-24 relative, are of the order of z's own rounding.
 __device__ __forceinline__ float act_sigmoid(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
 
+// The normal distribution's mass below z, 0.5 erfc(-z / sqrt 2), and e = exp(-z^2 / 2):
+// Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26 (erfc x =
+// poly(t) exp(-x^2), t = 1 / (1 + p x), x >= 0, off by at most 1.5e-7), halved;
+// the other side by symmetry. A third of erfcf's instructions, which bounded the
+// epilogue (E4M3 2049 x 14336 x 4096, gelu, fp32: 222 against 191 us).
+__device__ __forceinline__ float normal_mass(float z, float& e)
+{
+    const float x = 0.70710678118654752f * fabsf(z);
+    const float t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
+    e = __expf(-x * x);
+    float q = fmaf(0.5f * 1.061405429f, t, 0.5f * -1.453152027f);
+    q = fmaf(q, t, 0.5f * 1.421413741f);
+    q = fmaf(q, t, 0.5f * -0.284496736f);
+    q = fmaf(q, t, 0.5f * 0.254829592f) * t * e;
+    return z < 0.0f ? q : 1.0f - q;
+}
+
 // act(z) of the elementwise activations. gelu_tanh: 0.5 z (1 + tanh u) is z
-// times the logistic function of 2u; gelu: 0.5 z erfc(-z / sqrt 2), which does
-// not cancel for negative z.
+// times the logistic function of 2u.
 __device__ __forceinline__ float act_value(float z, int act)
 {
     switch (act) {
     case MXFP4_ACT_RELU:
         return z > 0.0f ? z : (z != z ? z : 0.0f);
-    case MXFP4_ACT_GELU:
-        return 0.5f * z * erfcf(-0.70710678118654752f * z);
+    case MXFP4_ACT_GELU: {
+        float e;
+        return z * normal_mass(z, e);
+    }
     case MXFP4_ACT_GELU_TANH:
         return z * act_sigmoid(1.5957691216057308f * (z + 0.044715f * z * z * z));
     case MXFP4_ACT_SILU:
@@ -192,8 +210,11 @@ __device__ __forceinline__ float act_slope(float z, int act)
     switch (act) {
     case MXFP4_ACT_RELU:
         return z > 0.0f ? 1.0f : (z != z ? z : 0.0f);
-    case MXFP4_ACT_GELU:
-        return 0.5f * erfcf(-0.70710678118654752f * z) + z * 0.39894228040143268f * expf(-0.5f * z * z);
+    case MXFP4_ACT_GELU: {
+        float e;
+        const float mass = normal_mass(z, e);
+        return mass + z * 0.39894228040143268f * e;
+    }
     case MXFP4_ACT_GELU_TANH: {
         if (fabsf(z) > 16.0f)  // saturated; z^2 must not overflow against a zero
             return z > 0.0f ? 1.0f : 0.0f;

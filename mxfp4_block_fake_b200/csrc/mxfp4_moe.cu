@@ -168,10 +168,15 @@ static mxfp4_status run_route(const mxfp4_moe_route_args* A, cudaStream_t s)
     const void* fn = nv == 1 ? route_fn<1>(b, g) : nv == 2 ? route_fn<2>(b, g) : nv == 4 ? route_fn<4>(b, g)
                      : nv == 8 ? route_fn<8>(b, g) : nv == 16 ? route_fn<16>(b, g) : route_fn<32>(b, g);
     mxfp4_status e = launch1(fn, r.chunks, RT_THREADS, smem, r, s);
-    if (e == MXFP4_OK && r.chunks > 1)
-        e = launch1((const void*)route_scan_kernel, (r.experts + 31) / 32, 1024, 0, r, s);
-    if (e == MXFP4_OK && r.chunks > 1)
-        e = launch1((const void*)route_place_kernel, r.chunks, RT_THREADS, 0, r, s);
+    if (e != MXFP4_OK || r.chunks == 1)
+        return e;
+    // every CTA reading all chunks' counts costs chunks^2 * experts words: up to
+    // 2^24 of them (about 3 us over the GPU) are cheaper than the scan's launch
+    if ((int64_t)r.chunks * r.chunks * r.experts <= (int64_t)1 << 24)
+        return launch1((const void*)route_place_kernel<true>, r.chunks, RT_THREADS, 0, r, s);
+    e = launch1((const void*)route_scan_kernel, (r.experts + 31) / 32, 1024, 0, r, s);
+    if (e == MXFP4_OK)
+        e = launch1((const void*)route_place_kernel<false>, r.chunks, RT_THREADS, 0, r, s);
     return e;
 }
 

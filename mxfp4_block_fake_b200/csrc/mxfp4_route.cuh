@@ -661,14 +661,45 @@ __global__ void __launch_bounds__(1024) route_scan_kernel(const RouteArgs a)
 }
 
 // Ranks within a chunk -> rows, and the rows' slots; -1 in the slots behind
-// the last row. One CTA per chunk.
+// the last row. One CTA per chunk. SCAN: the CTA adds up the chunks' counts
+// itself (few chunks: one launch instead of two); else ws holds the rows of
+// each expert before the chunk and `counts` the totals.
+template <bool SCAN>
 __global__ void __launch_bounds__(RT_THREADS) route_place_kernel(const RouteArgs a)
 {
-    __shared__ int s_cnt[RT_MAX_EXPERTS], s_off[RT_MAX_EXPERTS];
+    __shared__ int s_cnt[RT_MAX_EXPERTS], s_off[RT_MAX_EXPERTS], s_base[RT_MAX_EXPERTS];
     const int tid = threadIdx.x, E = a.experts, K = a.k;
-    for (int e = tid; e < E; e += RT_THREADS)
-        s_cnt[e] = (int)a.counts[e];
-    __syncthreads();
+    if constexpr (SCAN) {
+        // threads side by side on the chunks of one expert; integer sums, so their order does not matter
+        int segs = 1;
+        while (2 * segs * E <= RT_THREADS)
+            segs *= 2;
+        for (int e = tid; e < E; e += RT_THREADS)
+            s_cnt[e] = s_base[e] = 0;
+        __syncthreads();
+        for (int i = tid; i < segs * E; i += RT_THREADS) {
+            const int seg = i / E, e = i - seg * E;
+            int before = 0, total = 0;
+#pragma unroll 8
+            for (int c = seg; c < a.chunks; c += segs) {
+                const int v = a.ws[(int64_t)c * E + e];
+                total += v;
+                before += c < (int)blockIdx.x ? v : 0;
+            }
+            atomicAdd(&s_cnt[e], total);
+            atomicAdd(&s_base[e], before);
+        }
+        __syncthreads();
+        if (blockIdx.x == 0)
+            for (int e = tid; e < E; e += RT_THREADS)
+                a.counts[e] = s_cnt[e];
+    } else {
+        for (int e = tid; e < E; e += RT_THREADS) {
+            s_cnt[e] = (int)a.counts[e];
+            s_base[e] = a.ws[(int64_t)blockIdx.x * E + e];
+        }
+        __syncthreads();
+    }
     const int total = rt_scan(s_cnt, s_off, E);
     const int64_t p0 = (int64_t)blockIdx.x * RT_CHUNK * K;
     const int64_t pairs = a.tokens * K;
@@ -676,7 +707,7 @@ __global__ void __launch_bounds__(RT_THREADS) route_place_kernel(const RouteArgs
     for (int p = tid; p < n; p += RT_THREADS) {
         const int e = a.experts_out[p0 + p];
         if (e >= 0) {
-            const int r = a.rows[p0 + p] + a.ws[(int64_t)blockIdx.x * E + e] + s_off[e];
+            const int r = a.rows[p0 + p] + s_base[e] + s_off[e];
             a.rows[p0 + p] = r;
             a.slots[r] = (int)(p0 + p);
         }

@@ -638,14 +638,14 @@ def _rows2d(t: torch.Tensor, name: str, device: torch.device, dtype=None, shape=
         raise TypeError(f"{name} must be {dtype or 'float32 or bfloat16'}, got {t.dtype}")
     if shape is not None and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {list(t.shape)}, expected {list(shape)}")
-    return t if rows_addressable(t.shape, t.stride()) else t.contiguous()
+    return t if t.is_contiguous() or rows_addressable(t.shape, t.stride()) else t.contiguous()
 
 
 def _out2d(t: torch.Tensor | None, name: str, shape, dtype, device) -> torch.Tensor:
     """An output of this shape: a new tensor, or the caller's with unit column
     stride and rows that do not overlap."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(shape[0], shape[1], dtype=dtype, device=device)
     if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != dtype or tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must be a {dtype} CUDA tensor of shape {list(shape)} on {device}")
     if not rows_addressable(t.shape, t.stride()):
@@ -708,15 +708,14 @@ def mxfp4_moe_route(logits: torch.Tensor, k: int, *, score: str = "softmax", bia
         a.token_mask = token_mask.data_ptr()
     if k < 1 or k > e:
         raise ValueError(f"k must lie in [1, experts], got {k} of {e}")
-    i32 = dict(dtype=torch.int32, device=dev)
-    r = RouteResult(weights=torch.empty((t, k), dtype=torch.float32, device=dev), experts=torch.empty((t, k), **i32),
-                    rows=torch.empty((t, k), **i32), slots=torch.empty((t * k,), **i32),
-                    counts=torch.empty((e,), dtype=torch.int64, device=dev))
+    experts = torch.empty(t, k, dtype=torch.int32, device=dev)
+    r = RouteResult(torch.empty(t, k, dtype=torch.float32, device=dev), experts, torch.empty_like(experts),
+                    torch.empty(t * k, dtype=torch.int32, device=dev), torch.empty(e, dtype=torch.int64, device=dev))
     a.weights, a.chosen, a.rows = r.weights.data_ptr(), r.experts.data_ptr(), r.rows.data_ptr()
     a.slots, a.counts = r.slots.data_ptr(), r.counts.data_ptr()
     need = _abi.lib().mxfp4_moe_route_workspace(t, e)
     if need > 0:
-        ws = torch.empty((need,), dtype=torch.uint8, device=dev)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
         a.workspace, a.workspace_bytes = ws.data_ptr(), need
     _run(_abi.mxfp4_moe_route, a, dev, "mxfp4_moe_route")
     return r
@@ -777,16 +776,16 @@ def mxfp4_moe_dispatch(x: torch.Tensor, rows: torch.Tensor, *, emit_values: bool
     a.x, a.ld_tokens = x.data_ptr(), _ld(x)
     fmt = _elem_format(elem_format)
     width = cols if fmt == _abi.ELEM_E4M3 else (cols + 1) // 2
-    u8 = dict(dtype=torch.uint8, device=dev)
+    u8 = torch.uint8
     nbytes = scales_row_bytes(n, cols, 32, "mma") if emit_codes or (out is not None and out.codes is not None) else 0
     if out is None:
         if not emit_values and not emit_codes:
             raise ValueError("at least one of emit_values / emit_codes must be set")
         r = DispatchResult()
         if emit_values:
-            r.values = torch.empty((n, cols), dtype=x.dtype, device=dev)
+            r.values = torch.empty(n, cols, dtype=x.dtype, device=dev)
         if emit_codes:
-            r.codes, r.scales = torch.empty((n, width), **u8), torch.empty((nbytes,), **u8)
+            r.codes, r.scales = torch.empty(n, width, dtype=u8, device=dev), torch.empty(nbytes, dtype=u8, device=dev)
     else:
         r = out
         if r.values is None and r.codes is None:
@@ -806,7 +805,7 @@ def mxfp4_moe_dispatch(x: torch.Tensor, rows: torch.Tensor, *, emit_values: bool
         a.scale_factor = float(scale_factor)
         need = _abi.lib().mxfp4_moe_dispatch_workspace(t, a.k, cols, n)
         if need > 0:
-            ws = torch.empty((need,), **u8)
+            ws = torch.empty(need, dtype=u8, device=dev)
             a.workspace, a.workspace_bytes = ws.data_ptr(), need
     _run(_abi.mxfp4_moe_dispatch, a, dev, "mxfp4_moe_dispatch")
     return r
@@ -864,7 +863,7 @@ def mxfp4_moe_combine_bwd(grad_out: torch.Tensor, y: torch.Tensor | None, rows: 
     gy = gw = None
     if grad_weights:
         a.y, a.ld_rows = y.data_ptr(), _ld(y)
-        gw = torch.empty(rows.shape, dtype=torch.float32, device=dev)
+        gw = torch.empty_like(rows, dtype=torch.float32)
         a.grad_weights = gw.data_ptr()
     if grad_rows:
         gy = _out2d(out, "out", (n, cols), g.dtype, dev)
@@ -962,7 +961,7 @@ def mxfp4_grouped_linear(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tenso
         r.preact = _out2d(None if out is None else out.preact, "preact", (m, n), out_dtype, dev)
         g.preact, g.ld_preact = r.preact.data_ptr(), _ld(r.preact)
     if gl is not None:
-        r.status = torch.empty((1,), dtype=torch.int32, device=dev)
+        r.status = torch.empty(1, dtype=torch.int32, device=dev)
         g.status = r.status.data_ptr()
     _run(_abi.mxfp4_grouped_linear, g, dev, "mxfp4_grouped_linear")
     if gl is not None and (check is None or check):
@@ -994,12 +993,12 @@ def mxfp4_grouped_linear_bwd(grad_out: torch.Tensor, preact: torch.Tensor, group
     g.grad_preact, g.ld_grad = gz.data_ptr(), _ld(gz)
     gb = status = None
     if bias_grad:
-        gb = torch.empty((ng, n), dtype=torch.float32, device=dev)
+        gb = torch.empty(ng, n, dtype=torch.float32, device=dev)
         need = _abi.lib().mxfp4_grouped_linear_workspace(m, n, ng)
-        ws = torch.empty((need,), dtype=torch.uint8, device=dev)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
         g.grad_bias, g.workspace, g.workspace_bytes = gb.data_ptr(), ws.data_ptr(), need
     if gl is not None:
-        status = torch.empty((1,), dtype=torch.int32, device=dev)
+        status = torch.empty(1, dtype=torch.int32, device=dev)
         g.status = status.data_ptr()
     _run(_abi.mxfp4_grouped_linear_bwd, g, dev, "mxfp4_grouped_linear_bwd")
     if gl is not None and (check is None or check):
