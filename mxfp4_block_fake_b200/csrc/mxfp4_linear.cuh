@@ -161,6 +161,24 @@ __device__ int64_t ln_plan(const Args& a, int32_t* s_tpre, int32_t* s_rst)
     return build_plan<BS, true>(pa, s_tpre, s_rst);
 }
 
+// mbar_wait that reads the clock once in 64 tries: a read takes longer than the
+// event it would delay (a stage here is half a microsecond).
+__device__ __forceinline__ bool ln_wait(uint32_t bar, uint32_t parity)
+{
+    uint64_t t0 = 0;
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try(bar, parity))
+                return true;
+        const uint64_t now = global_ns();
+        if (t0 == 0)
+            t0 = now;
+        else if (now - t0 > SG_WAIT_NS)
+            return false;
+    }
+}
+
 // ---- activations -----------------------------------------------------------
 
 // 1 / (1 + e^-z) by the approximate exponential and quotient: their errors, a few
@@ -454,7 +472,7 @@ __global__ void __launch_bounds__(LnSmem<FMT, NT>::THREADS, 1) linear_kernel(con
                 okx |= (ok ? 1u : 0u) << q;
             }
             for (int ks = 0; ks < nst; ++ks) {
-                if (!__all_sync(FULL, mbar_wait(smem_addr(&sm.empty[s]), ph ^ 1u))) {
+                if (!__all_sync(FULL, ln_wait(smem_addr(&sm.empty[s]), ph ^ 1u))) {
                     sm.err = 1;
                     break;
                 }
@@ -495,7 +513,7 @@ __global__ void __launch_bounds__(LnSmem<FMT, NT>::THREADS, 1) linear_kernel(con
         if (lane == 0)
             for (int i = 0; i < S; ++i)
                 if (issued & (1u << i))
-                    (void)mbar_wait(smem_addr(&sm.full[i]), i < s ? ph : ph ^ 1u);
+                    (void)ln_wait(smem_addr(&sm.full[i]), i < s ? ph : ph ^ 1u);
         __syncwarp();
     } else if (warp == 1) {
         // ---- MMA issuer. The whole warp walks the tiles, so that addresses and
@@ -504,14 +522,14 @@ __global__ void __launch_bounds__(LnSmem<FMT, NT>::THREADS, 1) linear_kernel(con
         uint32_t ph = 0, aph = 0;
         for (int64_t t = blockIdx.x; t < tiles && !sm.err; t += gridDim.x) {
             const LnTile tl = ln_tile<NT>(a, s_tpre, s_rst, t, n_ft);
-            if (!__all_sync(FULL, mbar_wait(smem_addr(&sm.acc_empty[acc]), aph ^ 1u))) {
+            if (!__all_sync(FULL, ln_wait(smem_addr(&sm.acc_empty[acc]), aph ^ 1u))) {
                 sm.err = 1;
                 break;
             }
             gm_fence_after();
             const uint32_t d_tmem = tmem + (uint32_t)(acc * 2 * NT);
             for (int ks = 0; ks < nst; ++ks) {
-                if (!__all_sync(FULL, mbar_wait(smem_addr(&sm.full[s]), ph))) {
+                if (!__all_sync(FULL, ln_wait(smem_addr(&sm.full[s]), ph))) {
                     sm.err = 1;
                     break;
                 }
@@ -549,7 +567,7 @@ __global__ void __launch_bounds__(LnSmem<FMT, NT>::THREADS, 1) linear_kernel(con
         if (elect_one())
             gm_commit(smem_addr(&sm.done));
         __syncwarp();
-        (void)mbar_wait(smem_addr(&sm.done), 0);
+        (void)ln_wait(smem_addr(&sm.done), 0);
         __syncwarp();
     } else {
         // ---- epilogue: tensor-memory lanes 32 (warp % 4) .. + 31 of half h,
@@ -563,7 +581,7 @@ __global__ void __launch_bounds__(LnSmem<FMT, NT>::THREADS, 1) linear_kernel(con
             const int f = tl.f0 + 128 * h + 32 * quad + lane;
             const bool fok = f < a.n;
             const float bias = a.bias && fok ? a.bias[(int64_t)tl.g * a.n + f] : 0.0f;
-            if (!__all_sync(FULL, mbar_wait(smem_addr(&sm.acc_full[acc]), aph))) {
+            if (!__all_sync(FULL, ln_wait(smem_addr(&sm.acc_full[acc]), aph))) {
                 sm.err = 1;
                 break;
             }

@@ -541,6 +541,27 @@ def test_linear_epilogue(act, out, everything, fmt):
     linear_case([20, 0, 150, 3], 180, 262, 256, fmt, act=act, out=out, bias=everything, residual=everything, preact=everything)
 
 
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+@pytest.mark.parametrize("sizes,m", [([256], 256), ([300], 300), ([600, 0, 513, 1], 1200), ([257, 256, 255, 129, 640], 1537)])
+@pytest.mark.parametrize("n,k", [(256, 128), (257, 320), (640, 576), (1026, 256)])
+def test_linear_of_large_groups(fmt, sizes, m, n, k):
+    """Groups of several tiles: ragged groups, features and lengths."""
+    linear_case(sizes, m, n, k, fmt, act="swiglu" if n % 2 == 0 else "none", bias=True)
+
+
+@pytest.mark.parametrize("act", ["none", "relu", "gelu", "gelu_tanh", "silu", "swiglu"])
+@pytest.mark.parametrize("out", ["bf16", "fp32"])
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+def test_linear_epilogue_of_large_groups(act, out, fmt):
+    linear_case([300, 0, 470], 790, 390, 192, fmt, act=act, out=out, bias=True, residual=True, preact=True, list_type=0)
+
+
+def test_linear_many_tiles_of_large_groups():
+    linear_case([300, 700, 0, 64], 1064, 9000, 128, "e2m1", act="swiglu")
+    linear_case([600], 600, 11000, 64, "e2m1", out="fp32", dense=True)
+    linear_case([280, 260], 540, 9472, 160, "e4m3", residual=True)
+
+
 @pytest.mark.parametrize("n", [1, 2, 31, 127, 128, 129, 255, 256, 257, 384, 385])
 def test_linear_widths(n):
     linear_case([70, 9], 80, n, 192, "e2m1", out="fp32", bias=True, residual=True, preact=True)
