@@ -610,8 +610,8 @@ mxfp4_status mxfp4_moe_combine_bwd(const mxfp4_moe_move_args* args, mxfp4_stream
  * (0 for an empty group). The residual's gradient is grad_out; the
  * operands' gradients are grouped GEMMs of grad_preact. workspace:
  * mxfp4_grouped_linear_workspace(m, n, num_groups) bytes, 4-byte aligned,
- * when grad_bias is given. a, b and k are not used. Rows behind the last group
- * are left as they were.
+ * when grad_bias is given (num_groups 1 without a group list). a, b and k are
+ * not used. Rows behind the last group are left as they were.
  */
 typedef struct mxfp4_linear_args {
     int32_t elem_format;
@@ -644,6 +644,11 @@ typedef struct mxfp4_linear_args {
 } mxfp4_linear_args;
 
 mxfp4_status mxfp4_grouped_linear(const mxfp4_linear_args* args, mxfp4_stream_t stream);
+/* Bytes of workspace (16-byte aligned; its contents matter to the call only) with
+ * which the product that `args` describes runs faster; 0 where it would not, -1 for
+ * invalid arguments. Without it the product is formed all the same (its fp32 sums in
+ * another order). */
+int64_t mxfp4_grouped_linear_fwd_workspace(const mxfp4_linear_args* args);
 int64_t mxfp4_grouped_linear_workspace(int64_t m, int64_t n, int64_t num_groups);
 mxfp4_status mxfp4_grouped_linear_bwd(const mxfp4_linear_args* args, mxfp4_stream_t stream);
 

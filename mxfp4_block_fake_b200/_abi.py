@@ -47,6 +47,7 @@ EXPORTS = (
     "mxfp4_moe_combine",
     "mxfp4_moe_combine_bwd",
     "mxfp4_grouped_linear",
+    "mxfp4_grouped_linear_fwd_workspace",
     "mxfp4_grouped_linear_workspace",
     "mxfp4_grouped_linear_bwd",
     "mxfp4_status_string",
@@ -278,6 +279,8 @@ def lib() -> ctypes.CDLL:
     L.mxfp4_moe_route_workspace.restype = i64
     L.mxfp4_moe_dispatch_workspace.argtypes = [i64, i32, i64, i64]
     L.mxfp4_moe_dispatch_workspace.restype = i64
+    L.mxfp4_grouped_linear_fwd_workspace.argtypes = [ctypes.POINTER(LinearArgs)]
+    L.mxfp4_grouped_linear_fwd_workspace.restype = i64
     L.mxfp4_grouped_linear_workspace.argtypes = [i64, i64, i64]
     L.mxfp4_grouped_linear_workspace.restype = i64
     for name, struct in (("mxfp4_moe_route", RouteArgs), ("mxfp4_moe_route_bwd", RouteArgs),
@@ -380,3 +383,7 @@ def mxfp4_grouped_linear(args: LinearArgs, stream: int) -> int:
 
 def mxfp4_grouped_linear_bwd(args: LinearArgs, stream: int) -> int:
     return lib().mxfp4_grouped_linear_bwd(ctypes.byref(args), stream)
+
+
+def mxfp4_grouped_linear_fwd_workspace(args: LinearArgs) -> int:
+    return lib().mxfp4_grouped_linear_fwd_workspace(ctypes.byref(args))

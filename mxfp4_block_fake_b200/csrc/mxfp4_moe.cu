@@ -19,6 +19,7 @@ __device__ __forceinline__ uint32_t f32_to_bf16(float v) { return bf16x2(v, 0.0f
 #include "mxfp4_route.cuh"
 #include "mxfp4_permute.cuh"
 #include "mxfp4_linear.cuh"
+#include "mxfp4_linear2.cuh"
 
 namespace mxfp4 {
 
@@ -399,6 +400,102 @@ static mxfp4_status launch_linear_n(const mxfp4_linear_args* A, LnMaps maps, con
     return f32 ? launch_linear_t<FMT, NT, true>(maps, g, s) : launch_linear_t<FMT, NT, false>(maps, g, s);
 }
 
+// Clusters of `fn` that the device holds at once, cached per (device, kernel).
+static int resident_pairs(const void* fn, int threads, size_t smem)
+{
+    struct Entry {
+        const void* fn;
+        int dev;
+        size_t smem;
+        int pairs;
+    };
+    static Entry cache[64];
+    static int n = 0;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess)
+        return -1;
+    {
+        std::lock_guard<std::mutex> lk(g_mu);
+        for (int i = 0; i < n; ++i)
+            if (cache[i].fn == fn && cache[i].dev == dev && cache[i].smem == smem)
+                return cache[i].pairs;
+    }
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = dim3(2 * 1024);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = 2;
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    int pairs = 0;
+    if (cudaOccupancyMaxActiveClusters(&pairs, fn, &cfg) != cudaSuccess || pairs < 1)
+        return -1;
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (n < 64)
+        cache[n++] = Entry{fn, dev, smem, pairs};
+    return pairs;
+}
+
+// Bytes of the tokens' scales by tiles of the pair kernel.
+static int64_t scale_tiles_bytes(int64_t m, int64_t k, int64_t groups) { return (m / L2_NT + groups) * ((k + 127) / 128) * 1024; }
+
+template <int FMT, bool F32>
+static mxfp4_status launch_linear2(const mxfp4_linear_args* A, const LnMaps& maps, const LnArgs& g, int64_t kb, cudaStream_t s)
+{
+    using SM = Ln2Smem<FMT>;
+    const uint32_t atoms = SM::ATOMS;
+    const int64_t ncb = (g.k + 127) / 128;
+    Ln2Maps m2;
+    memset(&m2, 0, sizeof(m2));
+    m2.w = maps.w;
+    if (!encode_2d(&m2.x, CU_TENSOR_MAP_DATA_TYPE_UINT8, const_cast<uint8_t*>(A->a), (uint64_t)kb, (uint64_t)A->m,
+                   (uint64_t)A->lda, LN_ROW_BYTES, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !encode_2d(&m2.sfw, CU_TENSOR_MAP_DATA_TYPE_UINT32, const_cast<uint8_t*>(A->b_scales), 128,
+                   (uint64_t)(g.num_groups * (g.sfw_group_bytes >> 9)), 512, 128, atoms, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+        !encode_2d(&m2.sfx, CU_TENSOR_MAP_DATA_TYPE_UINT32, A->workspace, 128, (uint64_t)((g.m / L2_NT + g.num_groups) * ncb * 2), 512, 128,
+                   2 * atoms, CU_TENSOR_MAP_SWIZZLE_NONE))
+        return MXFP4_ECUDA;
+    const void* fn = (const void*)linear2_kernel<FMT, F32>;
+    const size_t plan = (size_t)(2 * (g.num_groups + 1)) * sizeof(int32_t), smem = sizeof(SM) + 1024 + plan;
+    if (!allow_smem(fn, smem))
+        return MXFP4_ECUDA;
+    const int pairs = resident_pairs(fn, L2_THREADS, smem);
+    if (pairs < 1)
+        return MXFP4_ECUDA;
+    const int64_t units = g.m / L2_NT + g.num_groups, bound = units * ((g.n + LN_FT - 1) / LN_FT);
+    LnArgs a = g;
+    uint32_t* ws = static_cast<uint32_t*>(A->workspace);
+    void* args1[] = {&a, &ws};
+    mxfp4_status st = launched(cudaLaunchKernel((const void*)scale_tiles_kernel, dim3((unsigned)(units < 4096 ? units : 4096), (unsigned)((ncb + SC_COLS - 1) / SC_COLS)),
+                                                dim3(L2_NT), args1, plan, s));
+    if (st != MXFP4_OK)
+        return st;
+    void* args2[] = {&m2, &a};
+    return launched(cudaLaunchKernel(fn, dim3((unsigned)(2 * (bound < pairs ? bound : pairs))), dim3(L2_THREADS), args2, smem, s));
+}
+
+// Whether a product goes to pairs of SMs (given the workspace). Groups that fill
+// 256-token tiles on average; tiles for most of the device (1024 x 4096 x 4096 31
+// against the single-SM kernel's 24 us, 4096 x 4096 x 4096 57 / 63); and eight
+// stages along K per bf16 stream of results and residuals: its one accumulator
+// does not hide a long epilogue (32768 x 4096 over 32 experts, E2M1, bf16 results:
+// k = 1024 184 / 160 us, 2048 194 / 194, 2560 203 / 226, 7168 391 / 486; E4M3 2049 x
+// 14336 x 4096, 32 stages: bf16 results 127 / 135, three fp32 streams 235 / 191).
+static bool linear_on_pairs(const mxfp4_linear_args* A)
+{
+    const int64_t stage = A->elem_format == MXFP4_ELEM_E2M1 ? LnFmt<MXFP4_ELEM_E2M1>::BK : LnFmt<MXFP4_ELEM_E4M3>::BK;
+    const int64_t groups = A->group_list ? A->num_groups : 1;
+    const int64_t streams = (1 + (A->preact != nullptr) + (A->residual != nullptr)) * (A->d_dtype == MXFP4_F32 ? 2 : 1);
+    return A->m / groups >= L2_NT && A->k >= 8 * stage * streams && (A->m / L2_NT) * (A->n / LN_FT) >= 128 &&
+           groups <= Ln2Smem<MXFP4_ELEM_E2M1>::MAX_GROUPS && scale_tiles_bytes(A->m, A->k, groups) / 512 <= INT32_MAX &&
+           groups * (mxfp4_scales_row_bytes(A->n, A->k, 32, MXFP4_SCALES_MMA) >> 9) <= INT32_MAX &&  // 32-bit coordinates
+           aligned(A->a_scales, 16);
+}
+
 template <int FMT>
 static mxfp4_status launch_linear(const mxfp4_linear_args* A, const LnMaps& maps, const LnArgs& g, int64_t kb, bool f32, cudaStream_t s)
 {
@@ -408,6 +505,8 @@ static mxfp4_status launch_linear(const mxfp4_linear_args* A, const LnMaps& maps
         return launch_linear_n<FMT, 32>(A, maps, g, kb, f32, s);
     if (mean <= 64 || g.num_groups > LnSmem<FMT, 128>::MAX_GROUPS)
         return launch_linear_n<FMT, 64>(A, maps, g, kb, f32, s);
+    if (linear_on_pairs(A) && A->workspace && A->workspace_bytes >= scale_tiles_bytes(g.m, g.k, g.num_groups))
+        return f32 ? launch_linear2<FMT, true>(A, maps, g, kb, s) : launch_linear2<FMT, false>(A, maps, g, kb, s);
     return launch_linear_n<FMT, 128>(A, maps, g, kb, f32, s);
 }
 
@@ -456,7 +555,7 @@ static mxfp4_status run_linear(const mxfp4_linear_args* A, cudaStream_t s)
     if (A->lda < kb || A->ldb < kb || A->lda % 16 != 0 || A->ldb % 16 != 0 || !aligned(A->a, 16) || !aligned(A->b, 16) ||
         !aligned(A->a_scales, 4) || !aligned(A->b_scales, 16))
         return MXFP4_EINVAL;
-    if (!aligned(A->y, esz) || !aligned(A->residual, esz) || !aligned(A->preact, esz) || !aligned(A->bias, 4) || !aligned(A->status, 4))
+    if (!aligned(A->y, esz) || !aligned(A->residual, esz) || !aligned(A->preact, esz) || !aligned(A->bias, 4) || !aligned(A->status, 4) || !aligned(A->workspace, 16))
         return MXFP4_EINVAL;
     LnArgs g;
     memset(&g, 0, sizeof(g));
@@ -602,6 +701,13 @@ mxfp4_status mxfp4_moe_combine_bwd(const mxfp4_moe_move_args* args, mxfp4_stream
 mxfp4_status mxfp4_grouped_linear(const mxfp4_linear_args* args, mxfp4_stream_t stream)
 {
     return run_linear(args, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int64_t mxfp4_grouped_linear_fwd_workspace(const mxfp4_linear_args* args)
+{
+    if (check_linear(args) != MXFP4_OK || args->k < 0)
+        return -1;
+    return linear_on_pairs(args) ? scale_tiles_bytes(args->m, args->k, args->group_list ? args->num_groups : 1) : 0;
 }
 
 int64_t mxfp4_grouped_linear_workspace(int64_t m, int64_t n, int64_t num_groups)

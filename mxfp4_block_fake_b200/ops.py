@@ -971,6 +971,10 @@ def mxfp4_grouped_linear(a: torch.Tensor, a_scales: torch.Tensor, b: torch.Tenso
     if gl is not None:
         r.status = _new((1,), torch.int32, dev)
         g.status = r.status.data_ptr()
+    need = _abi.mxfp4_grouped_linear_fwd_workspace(g)
+    if need > 0:
+        ws = _new((need,), torch.uint8, dev)
+        g.workspace, g.workspace_bytes = ws.data_ptr(), need
     _run(_abi.mxfp4_grouped_linear, g, dev, "mxfp4_grouped_linear")
     if gl is not None and (check is None or check):
         _check_status(r.status, "mxfp4_grouped_linear")

@@ -541,25 +541,51 @@ def test_linear_epilogue(act, out, everything, fmt):
     linear_case([20, 0, 150, 3], 180, 262, 256, fmt, act=act, out=out, bias=everything, residual=everything, preact=everything)
 
 
+def on_pairs(fmt, m, n, k, groups, streams=1):
+    a = ops._abi.LinearArgs()
+    a.elem_format, a.m, a.n, a.k, a.d_dtype = ops._elem_format(fmt), m, n, k, ops._abi.BF16
+    a.group_list, a.num_groups = 4096, groups        # not followed
+    a.preact = 4096 if streams > 1 else None
+    a.residual = 4096 if streams > 2 else None
+    return ops._abi.mxfp4_grouped_linear_fwd_workspace(a) > 0
+
+
 @pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
-@pytest.mark.parametrize("sizes,m", [([256], 256), ([300], 300), ([600, 0, 513, 1], 1200), ([257, 256, 255, 129, 640], 1537)])
-@pytest.mark.parametrize("n,k", [(256, 128), (257, 320), (640, 576), (1026, 256)])
+@pytest.mark.parametrize("sizes,m,n,k", [([300], 300, 640, 576), ([600, 0, 513, 1], 1200, 1026, 320), ([257, 256, 255, 129, 640], 1537, 256, 128),
+                                         ([8192], 8192, 1026, 2112), ([2000, 0, 4097, 1, 2300], 8500, 1026, 2176), ([257] * 9, 2400, 4096, 2048),
+                                         ([1000, 24, 5000, 0], 6300, 2050, 2304)])
 def test_linear_of_large_groups(fmt, sizes, m, n, k):
-    """Groups of several tiles: ragged groups, features and lengths."""
-    linear_case(sizes, m, n, k, fmt, act="swiglu" if n % 2 == 0 else "none", bias=True)
+    """Groups of several tiles: ragged groups, features and lengths; the larger
+    ones go to pairs of SMs, with more tiles than pairs."""
+    if m * n >= 128 * 65536:
+        assert on_pairs(fmt, m, n, k, len(sizes))
+    linear_case(sizes, m, n, k, fmt, act="swiglu" if n % 4 == 0 else "none", bias=True)
 
 
 @pytest.mark.parametrize("act", ["none", "relu", "gelu", "gelu_tanh", "silu", "swiglu"])
 @pytest.mark.parametrize("out", ["bf16", "fp32"])
 @pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
 def test_linear_epilogue_of_large_groups(act, out, fmt):
-    linear_case([300, 0, 470], 790, 390, 192, fmt, act=act, out=out, bias=True, residual=True, preact=True, list_type=0)
+    k = 2048 * 3 if fmt == "e2m1" else 1024 * 3 + 32
+    assert on_pairs(fmt, 4096, 2310, k, 3, streams=3)
+    linear_case([1300, 0, 2470], 4096, 2310, k * (2 if out == "fp32" else 1), fmt, act=act, out=out, bias=True, residual=True, preact=True, list_type=0)
 
 
-def test_linear_many_tiles_of_large_groups():
-    linear_case([300, 700, 0, 64], 1064, 9000, 128, "e2m1", act="swiglu")
-    linear_case([600], 600, 11000, 64, "e2m1", out="fp32", dense=True)
-    linear_case([280, 260], 540, 9472, 160, "e4m3", residual=True)
+def test_linear_with_and_without_its_workspace():
+    """The two kernels' fp32 sums differ by their order only."""
+    m, n, k = 4096, 2304, 4096
+    a, sa = operand(m, k, "e2m1", 1)
+    b, sb = operand(n, k, "e2m1", 2, 117, 119)
+    args = (a.cuda(), sa.cuda(), b.cuda(), sb.cuda())
+    one = ops.mxfp4_grouped_linear(*args, k=k, out_dtype=torch.float32).y
+    A = ops._abi.LinearArgs()
+    two = torch.empty_like(one)
+    A.m, A.n, A.k, A.d_dtype = m, n, k, ops._abi.F32
+    A.a, A.lda, A.a_scales = args[0].data_ptr(), k // 2, args[1].data_ptr()
+    A.b, A.ldb, A.b_scales = args[2].data_ptr(), k // 2, args[3].data_ptr()
+    A.y, A.ld_y = two.data_ptr(), n
+    assert ops._abi.mxfp4_grouped_linear(A, torch.cuda.current_stream().cuda_stream) == 0
+    assert (one - two).norm() <= 2 * k * U32 * one.norm()
 
 
 @pytest.mark.parametrize("n", [1, 2, 31, 127, 128, 129, 255, 256, 257, 384, 385])

@@ -165,6 +165,16 @@ def test_workspace_sizes(abi):
     assert L.mxfp4_moe_route_workspace(-1, 4) == -1
     assert L.mxfp4_grouped_linear_workspace(130, 10, 3) == (4 + 3) * 10 * 4
     assert L.mxfp4_grouped_linear_workspace(130, 10, 0) == -1
+    ws = abi.mxfp4_grouped_linear_fwd_workspace
+    big = dict(m=8192, n=4096, k=7168, num_groups=8)
+    assert ws(linear(abi, **{**big, "m": 8})) == 0
+    assert ws(linear(abi, **big)) == (32 + 8) * 56 * 1024
+    assert ws(linear(abi, **{**big, "k": 1024})) == 0
+    assert ws(linear(abi, **{**big, "group_list": None})) == (32 + 1) * 56 * 1024
+    assert ws(linear(abi, **{**big, "activation": 9})) == -1
+    assert L.mxfp4_moe_dispatch_workspace(4, 8, 7168, 32) == 0
+    assert L.mxfp4_moe_dispatch_workspace(8192, 8, 7168, 65536) == (8192 * 56 + 65536) * 4
+    assert L.mxfp4_moe_dispatch_workspace(-1, 8, 7168, 1) == -1
 
 
 def test_cpu_tensors_are_refused():
