@@ -6,9 +6,11 @@ Layers:
   _abi                ctypes mirror of the C ABI
   ops                 the entry points over torch CUDA tensors
   qat                 autograd STE function, quantizer module, QAT Linear
+  moe                 differentiable routing, dispatch, combine and grouped linear; MoE module
   workloads           seeded synthetic inputs
 """
 from ._abi import MXFP4ArgumentError, MXFP4Error
+from .moe import MXFP4MoE, moe_combine, moe_dispatch, moe_expert_operands, moe_grouped_linear, moe_route
 from .ops import (
     DispatchResult,
     DualLevelResult,
@@ -47,5 +49,6 @@ __all__ = [
     "MXFP4QATLinear", "convert_to_mxfp4_qat", "mxfp4_fake_quant", "mxfp4_quant_dequant",
     "mxfp4_saturation_mask", "unpack_mask", "DispatchResult", "LinearResult", "RouteResult", "mxfp4_grouped_gemm",
     "mxfp4_grouped_linear", "mxfp4_grouped_linear_bwd", "mxfp4_moe_combine", "mxfp4_moe_combine_bwd",
-    "mxfp4_moe_dispatch", "mxfp4_moe_route", "mxfp4_moe_route_bwd",
+    "mxfp4_moe_dispatch", "mxfp4_moe_route", "mxfp4_moe_route_bwd", "MXFP4MoE", "moe_combine", "moe_dispatch",
+    "moe_expert_operands", "moe_grouped_linear", "moe_route",
 ]

@@ -1,0 +1,122 @@
+"""GPU checks of the mixture-of-experts module API (moe.py): values and
+gradients against autograd of the same layer in 64 bits on the fake-quantised
+values, and the serving form against the training one."""
+from __future__ import annotations
+
+import pytest
+import torch
+
+from mxfp4_block_fake_b200 import MXFP4MoE, moe, mxfp4_quant_dequant, ops
+from tests import moe_ref as R
+
+pytestmark = pytest.mark.gpu
+
+U32, U16 = 2.0 ** -24, 2.0 ** -8
+
+
+def rnd(*shape, seed=0, std=1.0, dtype=torch.float32):
+    return (torch.randn(*shape, generator=torch.Generator().manual_seed(seed)) * std).to(dtype).cuda()
+
+
+def ste(v: torch.Tensor) -> torch.Tensor:
+    """Quantised value, gradient passed through (64 bits)."""
+    return v + (mxfp4_quant_dequant(v.detach().float()).double() - v.detach())
+
+
+@pytest.mark.parametrize("masked", [False, True])
+def test_gradients_of_the_functions(masked):
+    """fp32 throughout, so that only fp32 roundings separate the two (each
+    result is a chain of sums of at most 192 products): norms within 4 * 192
+    roundings."""
+    t, cols, n, experts, k = 70, 128, 192, 5, 2
+    x, lg, w, b = (rnd(t, cols, seed=1), rnd(t, experts, seed=2), rnd(experts, n, cols, seed=3, std=0.1), rnd(experts, n, seed=4))
+    go = rnd(t, n // 2, seed=5)
+    res = rnd(t, n // 2, seed=6)
+    mask = (torch.arange(t) % 7 != 0).cuda() if masked else None
+    leaves = [v.clone().requires_grad_(True) for v in (x, lg, w, b, res)]
+    r = moe.moe_route(leaves[1], k, score="sigmoid", token_mask=mask)
+    y = moe.moe_grouped_linear(moe.moe_dispatch(leaves[0], r), leaves[2], r.counts, leaves[3], activation="swiglu")
+    out = moe.moe_combine(y, r, residual=leaves[4])
+    out.backward(go)
+    ref = [v.double().requires_grad_(True) for v in (x, lg, w, b, res)]
+    weights = R.route_weights(ref[1], r.experts, "sigmoid", True, 1.0)
+    xq, wq = ste(ref[0]), ste(ref[2])
+    want = ref[4].clone()
+    for j in range(k):
+        e = r.experts[:, j].long().clamp(min=0)
+        z = torch.einsum("tk,tnk->tn", xq, wq[e]) + ref[3][e]
+        want = want + (weights[:, j] * (r.experts[:, j] >= 0))[:, None] * R.activation(z, "swiglu")
+    want.backward(go.double())
+    for got, exp in ((out, want), *((a.grad, c.grad) for a, c in zip(leaves, ref))):
+        assert (got.double() - exp).norm() <= 4 * 192 * U32 * exp.norm()
+
+
+@pytest.mark.parametrize("tokens", [1, 33, 700])
+def test_module_serves_what_it_trains(tokens):
+    """Laid out for serving, the layer gives the training forward's bytes: the same codes go through the same kernels."""
+    torch.manual_seed(0)
+    m = MXFP4MoE(256, 128, 8, 3, score="sigmoid", num_groups=4, topk_groups=2, balance=True, device="cuda")
+    x = rnd(2, tokens, 256, seed=7, dtype=torch.bfloat16)
+    mask = torch.ones(2, tokens, dtype=torch.bool, device="cuda")
+    mask[1, tokens // 2:] = False
+    out, counts = m(x, mask, return_counts=True)
+    assert out.requires_grad and int(counts.sum()) == 3 * int(mask.sum())
+    assert torch.equal(out[~mask], x[~mask])
+    m.lay_out()
+    with torch.no_grad():
+        assert torch.equal(m(x, mask), out)
+    m.update_balance(counts)
+    low = counts.float() < counts.float().mean()
+    assert bool((m.balance[low] > 0).all()) and bool((m.balance[~low] <= 0).all())
+    out.sum().backward()
+    for p in m.parameters():
+        assert p.grad is not None and bool(torch.isfinite(p.grad).all()) and float(p.grad.abs().sum()) > 0
+
+
+def test_module_in_a_graph():
+    """The serving forward captured and replayed while eager training goes on."""
+    torch.manual_seed(1)
+    m = MXFP4MoE(128, 64, 4, 2, device="cuda").lay_out()
+    xs = [rnd(40, 128, seed=i, dtype=torch.bfloat16) for i in range(3)]
+    with torch.no_grad():
+        want = [m(v) for v in xs]
+        static = xs[0].clone()
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            m(static)
+        torch.cuda.current_stream().wait_stream(side)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = m(static)
+    for v, w in zip(xs, want):
+        static.copy_(v)
+        g.replay()
+        m(v).sum().backward()
+        assert torch.equal(out, w)
+
+
+def test_optimiser_steps_run():
+    torch.manual_seed(2)
+    m = MXFP4MoE(64, 64, 4, 2, device="cuda", dtype=torch.float32)
+    opt = torch.optim.SGD(m.parameters(), lr=1e-2)
+    before = [p.detach().clone() for p in m.parameters()]
+    for i in range(2):
+        opt.zero_grad()
+        m(rnd(50, 64, seed=i)).square().mean().backward()
+        opt.step()
+    assert all(bool(torch.isfinite(p).all()) and not torch.equal(p, q) for p, q in zip(m.parameters(), before))
+
+
+def test_refusals():
+    with pytest.raises(ValueError):
+        MXFP4MoE(100, 64, 4, 2)
+    with pytest.raises(ValueError):
+        MXFP4MoE(64, 64, 4, 2, scale_mode="ceil")
+    with pytest.raises(ValueError):
+        moe.moe_grouped_linear(rnd(4, 64), rnd(2, 8, 128), torch.tensor([2, 2]).cuda())
+    m = MXFP4MoE(64, 64, 4, 2, device="cuda")
+    with pytest.raises(ValueError):
+        m.update_balance(torch.zeros(4, device="cuda"))
+    with pytest.raises(ValueError):
+        m(torch.zeros(3, 64, dtype=torch.bfloat16, device="cuda"), torch.ones(2, dtype=torch.bool, device="cuda"))
