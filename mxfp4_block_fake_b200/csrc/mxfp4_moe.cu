@@ -115,12 +115,12 @@ static mxfp4_status route_args(const mxfp4_moe_route_args* A, RouteArgs* r)
     return MXFP4_OK;
 }
 
-template <int NV>
+template <int NV, int LW>
 static const void* route_fn(bool bf16, bool sigmoid)
 {
     if (sigmoid)
-        return bf16 ? (const void*)route_kernel<NV, true, true> : (const void*)route_kernel<NV, false, true>;
-    return bf16 ? (const void*)route_kernel<NV, true, false> : (const void*)route_kernel<NV, false, false>;
+        return bf16 ? (const void*)route_kernel<NV, true, true, LW> : (const void*)route_kernel<NV, false, true, LW>;
+    return bf16 ? (const void*)route_kernel<NV, true, false, LW> : (const void*)route_kernel<NV, false, false, LW>;
 }
 
 static mxfp4_status run_route(const mxfp4_moe_route_args* A, cudaStream_t s)
@@ -158,16 +158,21 @@ static mxfp4_status run_route(const mxfp4_moe_route_args* A, cudaStream_t s)
     r.top2 = A->group_score == MXFP4_GROUP_TOP2;
     r.chunks = (int32_t)route_chunks(A->tokens);
     const size_t smem = (size_t)RT_WARPS * r.experts * 8 + (size_t)r.experts * 8 + (size_t)RT_CHUNK * r.k * 2;
-    int nv = 1;  // experts per lane
-    while (32 * nv < r.experts)
+    // two tokens a warp where sixteen lanes hold eight experts each, the choices
+    // and the groups (65536 tokens: 128 experts, k = 8 67 against 77 us with one
+    // token, 64 experts, k = 6 53 / 64; with 256 experts, sixteen a lane, 133 / 101)
+    const bool half = r.experts <= 128 && r.k < 16 && r.groups <= 16;
+    int nv = half ? 4 : 1;  // experts per lane
+    while ((half ? 16 : 32) * nv < r.experts)
         nv *= 2;
     r.per = r.experts / r.groups;
     r.per_magic = r.per == 1 ? 0u : (uint32_t)((0x100000000ull + r.per - 1) / r.per);
     r.lanes = r.per % nv == 0 && ((r.per / nv) & (r.per / nv - 1)) == 0 ? r.per / nv : 0;
     r.vec = r.experts % nv == 0 && aligned(A->logits, 16) && (A->ld * (int64_t)esz) % 16 == 0;
     const bool b = r.bf16, g = r.sigmoid;
-    const void* fn = nv == 1 ? route_fn<1>(b, g) : nv == 2 ? route_fn<2>(b, g) : nv == 4 ? route_fn<4>(b, g)
-                     : nv == 8 ? route_fn<8>(b, g) : nv == 16 ? route_fn<16>(b, g) : route_fn<32>(b, g);
+    const void* fn = half ? (nv == 4 ? route_fn<4, 16>(b, g) : route_fn<8, 16>(b, g))
+                     : nv == 1 ? route_fn<1, 32>(b, g) : nv == 2 ? route_fn<2, 32>(b, g) : nv == 4 ? route_fn<4, 32>(b, g)
+                     : nv == 8 ? route_fn<8, 32>(b, g) : nv == 16 ? route_fn<16, 32>(b, g) : route_fn<32, 32>(b, g);
     mxfp4_status e = launch1(fn, r.chunks, RT_THREADS, smem, r, s);
     if (e != MXFP4_OK || r.chunks == 1)
         return e;

@@ -3,8 +3,8 @@
 // mxfp4_moe.cu; the definition is in include/mxfp4.h, mxfp4_moe_route).
 //
 // Selection is decided by real numbers (the keys s_e + b_e), so it must not
-// depend on how an exponential happens to round. A warp takes a token, a lane
-// NV consecutive experts; keys are formed in fp32 with the approximate
+// depend on how an exponential happens to round. A warp takes a token (or two, one per
+// half), a lane NV consecutive experts; keys are formed in fp32 with the approximate
 // exponential, and every comparison the answer rests on (between neighbours in
 // the sorted choice, at its end, and between the last group kept and the first
 // dropped) is checked against the keys' error bound. A token with a comparison
@@ -84,6 +84,45 @@ __device__ __forceinline__ float rcp_approx(float v)
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
     return r;
+}
+
+// Reductions over the LW lanes (32, or 16: two tokens a warp) of a token.
+template <int LW>
+__device__ __forceinline__ float part_max(float v)
+{
+    if constexpr (LW == 32)
+        return warp_max(v);
+#pragma unroll
+    for (int o = LW / 2; o; o >>= 1)
+        v = max_nan(v, __shfl_xor_sync(FULL, v, o));
+    return v;
+}
+
+template <int LW>
+__device__ __forceinline__ uint32_t part_max(uint32_t v)
+{
+    if constexpr (LW == 32)
+        return __reduce_max_sync(FULL, v);
+#pragma unroll
+    for (int o = LW / 2; o; o >>= 1)
+        v = max(v, __shfl_xor_sync(FULL, v, o));
+    return v;
+}
+
+template <int LW>
+__device__ __forceinline__ float part_sum(float v)
+{
+#pragma unroll
+    for (int o = LW / 2; o; o >>= 1)
+        v += __shfl_xor_sync(FULL, v, o);
+    return v;
+}
+
+template <int LW>
+__device__ __forceinline__ uint32_t part_ballot(bool p)
+{
+    const uint32_t b = __ballot_sync(FULL, p);
+    return LW == 32 ? b : (b >> (threadIdx.x & 16)) & 0xFFFFu;
 }
 
 template <typename T>
@@ -199,10 +238,10 @@ __device__ __forceinline__ float rt_unorder(uint32_t u)
 }
 
 // The NV logits of this lane (experts lane * NV ..): -inf behind the last expert.
-template <int NV, bool BF16>
+template <int NV, bool BF16, int LW>
 __device__ __forceinline__ void rt_load(const RouteArgs& a, int64_t t, float (&x)[NV])
 {
-    const int e0 = (threadIdx.x & 31) * NV;
+    const int e0 = (threadIdx.x & (LW - 1)) * NV;
     const int64_t i0 = t * a.ld + e0;
     if constexpr (NV * (BF16 ? 2 : 4) >= 16) {
         if (a.vec) {
@@ -285,11 +324,11 @@ __device__ __forceinline__ float rt_key_error(float s, float key)
 // scratch of a.experts doubles; xe receives the choice's logit. Each lane sorts its keys once, as
 // order-preserving words whose low bits hold the lane's index (the lower expert
 // first); the k rounds then take the largest head and shift one lane's list.
-template <int NV, bool BF16, bool SIG>
-__device__ __forceinline__ int rt_select(const RouteArgs& a, int64_t t, const float (&x)[NV], const float (&b)[NV], float bm,
+template <int NV, bool BF16, bool SIG, int LW>
+__device__ __forceinline__ int rt_select(const RouteArgs& a, int t, bool live, const float (&x)[NV], const float (&b)[NV], float bm,
                                          bool exact, float m, double* s_key, float& xe)
 {
-    const int lane = threadIdx.x & 31, K = a.k;
+    const int lane = threadIdx.x & (LW - 1), K = a.k;
     constexpr uint32_t INDEX = NV - 1;
     float key[NV], r = 1.0f;
     bool unsure = false;
@@ -303,7 +342,7 @@ __device__ __forceinline__ int rt_select(const RouteArgs& a, int64_t t, const fl
 #pragma unroll
             for (int i = 0; i < NV; ++i)
                 total += rt_score<false>(x[i], m, 1.0f);
-            r = rcp_approx(warp_sum(total));
+            r = rcp_approx(part_sum<LW>(total));
         }
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
@@ -325,10 +364,10 @@ __device__ __forceinline__ int rt_select(const RouteArgs& a, int64_t t, const fl
                 next = fmaxf(fminf(best, ob), fmaxf(next, on));
                 best = fmaxf(best, ob);
             }
-            best = __shfl_sync(FULL, best, (lane * a.lanes) & 31);
-            next = __shfl_sync(FULL, next, (lane * a.lanes) & 31);
+            best = __shfl_sync(FULL, best, (lane * a.lanes) & (LW - 1), LW);
+            next = __shfl_sync(FULL, next, (lane * a.lanes) & (LW - 1), LW);
         } else {
-            float* s = reinterpret_cast<float*>(s_key);
+            float* s = reinterpret_cast<float*>(s_key) + ((threadIdx.x & 31) / LW) * a.experts;
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < NV; ++i)
@@ -348,25 +387,31 @@ __device__ __forceinline__ int rt_select(const RouteArgs& a, int64_t t, const fl
             rank += next;
         int before = 0;  // groups ahead of this lane's (lane g: group g)
         if (a.groups <= 8) {
-            // lane (g, quarter): two comparisons of the eight of group g
-            const int g = lane & 7, h = (lane >> 3) * 2;
-            const float mine = __shfl_sync(FULL, rank, g), r0 = __shfl_sync(FULL, rank, h), r1 = __shfl_sync(FULL, rank, h + 1);
-            before = (int)(r0 > mine || (r0 == mine && h < g)) + (int)(r1 > mine || (r1 == mine && h + 1 < g));
-            before += __shfl_xor_sync(FULL, before, 8);
-            before += __shfl_xor_sync(FULL, before, 16);
+            // lane (g, part): its share of the eight comparisons of group g
+            constexpr int SHARE = 64 / LW;
+            const int g = lane & 7, h = (lane >> 3) * SHARE;
+            const float mine = __shfl_sync(FULL, rank, g, LW);
+#pragma unroll
+            for (int q = 0; q < SHARE; ++q) {
+                const float rq = __shfl_sync(FULL, rank, h + q, LW);
+                before += (int)(rq > mine || (rq == mine && h + q < g));
+            }
+#pragma unroll
+            for (int o = 8; o < LW; o <<= 1)
+                before += __shfl_xor_sync(FULL, before, o);
         } else {
 #pragma unroll 4
             for (int g = 0; g < a.groups; ++g) {
-                const float rg = __shfl_sync(FULL, rank, g);
+                const float rg = __shfl_sync(FULL, rank, g, LW);
                 before += rg > rank || (rg == rank && g < lane);
             }
         }
         const bool keep = lane < a.groups && before < a.topk_groups;
-        kept = __ballot_sync(FULL, keep);
+        kept = part_ballot<LW>(keep);
         if (!exact || a.top2) {
             // the least rank kept against the greatest dropped: a rank is one or
             // two keys, whose scores are at most 1 and sum to |rank| + 2 bm
-            const float low = -warp_max(keep ? -rank : -INFINITY), high = warp_max(keep ? -INFINITY : rank);
+            const float low = -part_max<LW>(keep ? -rank : -INFINITY), high = part_max<LW>(keep ? -INFINITY : rank);
             const float size = fmaxf(fabsf(low), fabsf(high)) + 2.0f * bm;
             const float err = fminf(size, 2.0f) * (SIG ? 0x1p-19f : 0x1p-17f) + size * 0x1p-22f + 0x1p-24f;
             unsure = high > -INFINITY && low - high <= 2.0f * err;
@@ -396,12 +441,13 @@ __device__ __forceinline__ int rt_select(const RouteArgs& a, int64_t t, const fl
     int src = 0;          // and its lane
     for (int j = 0; j <= K; ++j) {
         // equal keys: the lowest lane holds the lowest expert
-        const uint32_t head = v[0] & ~INDEX, top = __reduce_max_sync(FULL, head);
-        if (top <= CLOSED)
+        const uint32_t head = v[0] & ~INDEX, top = part_max<LW>(head);
+        const bool some = top > CLOSED;
+        if (!__any_sync(FULL, some))
             break;
-        const int at = __ffs(__ballot_sync(FULL, head == top)) - 1;
-        const uint32_t taken = __shfl_sync(FULL, v[0], at);
-        if (lane == j) {
+        const int at = __ffs(part_ballot<LW>(some && head == top)) - 1;  // -1: nothing is left to this token
+        const uint32_t taken = __shfl_sync(FULL, v[0], at & (LW - 1), LW);
+        if (lane == j && some) {
             word = taken;
             src = at;
         }
@@ -417,9 +463,9 @@ __device__ __forceinline__ int rt_select(const RouteArgs& a, int64_t t, const fl
     xe = e >= 0 ? rt_logit<BF16>(a, t, e) : -INFINITY;
     if (!(exact && BF16)) {
         const float be = e >= 0 && a.bias ? a.bias[e] : 0.0f;
-        const float xn = __shfl_down_sync(FULL, xe, 1), bn = __shfl_down_sync(FULL, be, 1);
-        const int en = __shfl_down_sync(FULL, e, 1);
-        const uint32_t wn = __shfl_down_sync(FULL, word, 1);
+        const float xn = __shfl_down_sync(FULL, xe, 1, LW), bn = __shfl_down_sync(FULL, be, 1, LW);
+        const int en = __shfl_down_sync(FULL, e, 1, LW);
+        const uint32_t wn = __shfl_down_sync(FULL, word, 1, LW);
         bool close;
         if (exact) {
             close = lane < K - 1 ? !(xe > xn || (xe == xn && e < en)) : ((word ^ wn) & ~INDEX) == 0u;
@@ -432,12 +478,21 @@ __device__ __forceinline__ int rt_select(const RouteArgs& a, int64_t t, const fl
             if (lane < K - 1 && xe == xn && be == bn)
                 close = e > en;  // equal keys: the lower expert first
         }
-        // a lane whose successor exists; the 32nd choice's is not at hand
-        unsure = unsure || (lane < K && e >= 0 && (K < 32 || lane < 31 ? en >= 0 && close : true));
+        // a lane whose successor exists; that of a choice in the last lane is not at hand
+        unsure = unsure || (lane < K && e >= 0 && (K < LW || lane < LW - 1 ? en >= 0 && close : true));
     }
     int mine = lane < K ? e : -1;
-    if (__any_sync(FULL, unsure)) {
-        mine = rt_select64(a, t, s_key, m, exact);
+    const uint32_t again = __ballot_sync(FULL, unsure && live);
+    if (again) {  // the warp's tokens in doubt, one by one
+#pragma unroll 1
+        for (int h = 0; h < 32; h += LW)
+            if ((again >> h) & (LW == 32 ? 0xFFFFFFFFu : 0xFFFFu)) {
+                const int th = __shfl_sync(FULL, t, h);
+                const float mh = __shfl_sync(FULL, m, h);
+                const int got = __shfl_sync(FULL, rt_select64(a, th, s_key, mh, exact), lane);
+                if ((int)(threadIdx.x & 31 & ~(LW - 1)) == h)
+                    mine = got;
+            }
         xe = mine >= 0 ? rt_logit<BF16>(a, t, mine) : -INFINITY;
     }
     if (mine < 0)
@@ -451,12 +506,13 @@ __device__ __forceinline__ int rt_select(const RouteArgs& a, int64_t t, const fl
 __device__ __forceinline__ float rt_sigmoid(float x) { return __fdividef(1.0f, 1.0f + expf(-x)); }
 
 // Sum over the k slots' lanes (0 in the others).
+template <int LW>
 __device__ __forceinline__ float rt_sum_k(const RouteArgs& a, float v)
 {
-    if (a.k > 8) {
-        v += __shfl_xor_sync(FULL, v, 16);
-        v += __shfl_xor_sync(FULL, v, 8);
-    }
+    if (a.k > 8)
+#pragma unroll
+        for (int o = LW / 2; o >= 8; o >>= 1)
+            v += __shfl_xor_sync(FULL, v, o);
 #pragma unroll
     for (int o = 4; o; o >>= 1)
         v += __shfl_xor_sync(FULL, v, o);
@@ -464,11 +520,12 @@ __device__ __forceinline__ float rt_sum_k(const RouteArgs& a, float v)
 }
 
 // x: the choice's logit, -inf where there is none.
+template <int LW>
 __device__ __forceinline__ float rt_weight(const RouteArgs& a, int mine, float x, float m, float sum)
 {
     float s;
     if (a.renorm) {
-        const float top = warp_max(x);
+        const float top = part_max<LW>(x);
         if (a.sigmoid) {
             const float shift = top < -60.0f ? top : 0.0f;  // below that 1 + e^x is 1
             s = top < -60.0f ? expf(x - shift) : rt_sigmoid(x);
@@ -476,7 +533,7 @@ __device__ __forceinline__ float rt_weight(const RouteArgs& a, int mine, float x
             s = expf(x - top);
         }
         s = mine >= 0 ? s : 0.0f;
-        const float total = rt_sum_k(a, s);
+        const float total = rt_sum_k<LW>(a, s);
         return total > 0.0f ? a.scale * __fdividef(s, total) : 0.0f;
     }
     s = a.sigmoid ? rt_sigmoid(x) : expf(x - m) / sum;
@@ -519,12 +576,12 @@ __device__ int rt_scan(const int* s_cnt, int* s_off, int n)
 
 // One CTA per chunk. A single chunk (chunks == 1) finishes the order itself;
 // else `rows` receives ranks within the chunk and ws the chunk's counts.
-template <int NV, bool BF16, bool SIG>
-__global__ void __launch_bounds__(RT_THREADS, NV <= 8 ? 4 : 1) route_kernel(const __grid_constant__ RouteArgs a)
+template <int NV, bool BF16, bool SIG, int LW>
+__global__ void __launch_bounds__(RT_THREADS, NV <= 8 ? 4 : NV == 16 ? 2 : 1) route_kernel(const __grid_constant__ RouteArgs a)
 {
     extern __shared__ __align__(16) uint8_t rt_dyn[];
     const int E = a.experts, K = a.k;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & (LW - 1), warp = tid >> 5;
     double* s_key = reinterpret_cast<double*>(rt_dyn) + (size_t)warp * E;
     uint32_t* s_bits = reinterpret_cast<uint32_t*>(rt_dyn + (size_t)RT_WARPS * E * 8);  // [E][2]
     int16_t* s_pick = reinterpret_cast<int16_t*>(s_bits + 2 * E);                       // [RT_CHUNK][K]
@@ -559,34 +616,49 @@ __global__ void __launch_bounds__(RT_THREADS, NV <= 8 ? 4 : 1) route_kernel(cons
         for (int i = 0; i < NV; ++i)
             b[i] = 0.0f;
     }
-    for (int i = warp; i < nt; i += RT_WARPS) {
+    constexpr int TOKENS = 32 / LW;  // of a warp at a time
+    for (int i0 = warp * TOKENS; i0 < nt; i0 += RT_WARPS * TOKENS) {
+        const int i = i0 + (tid & 31) / LW;
         const int64_t t = t0 + i;
-        int mine = -1;
-        float w = 0.0f;
-        if (!a.token_mask || a.token_mask[t]) {
-            rt_load<NV, BF16>(a, t, x);
-            float m = x[0];
+        const bool here = i < nt, active = here && (!a.token_mask || a.token_mask[t]);
+        float m = -INFINITY;
+        if (active) {
+            rt_load<NV, BF16, LW>(a, t, x);
+            m = x[0];
 #pragma unroll
             for (int e = 1; e < NV; ++e)
                 m = max_nan(m, x[e]);
-            m = warp_max(m);
-            if (!(m < INFINITY)) {  // a NaN or +inf
-                mine = lane < K ? lane : -1;
-                w = __uint_as_float(QNAN32);
-            } else if (m > -INFINITY) {
-                float sum = 0.0f;
-                if (!SIG && !a.renorm) {
+        }
+        __syncwarp();
+        m = part_max<LW>(m);
+        const bool bad = active && !(m < INFINITY);  // a NaN or +inf
+        const bool live = active && !bad && m > -INFINITY;
+        int mine = bad && lane < K ? lane : -1;
+        float w = bad ? __uint_as_float(QNAN32) : 0.0f;
+        if (__any_sync(FULL, live)) {
+            if (!live) {
+                m = 0.0f;
 #pragma unroll
-                    for (int e = 0; e < NV; ++e)
-                        sum += expf(x[e] - m);
-                    sum = warp_sum(sum);
-                }
-                float xe;
-                mine = rt_select<NV, BF16, SIG>(a, t, x, b, bm, exact, m, s_key, xe);
-                w = rt_weight(a, mine, xe, m, sum);
+                for (int e = 0; e < NV; ++e)
+                    x[e] = -INFINITY;
+            }
+            __syncwarp();
+            float sum = 0.0f;
+            if (!SIG && !a.renorm) {
+#pragma unroll
+                for (int e = 0; e < NV; ++e)
+                    sum += expf(x[e] - m);
+                sum = part_sum<LW>(sum);
+            }
+            float xe;
+            const int got = rt_select<NV, BF16, SIG, LW>(a, live ? (int)t : (int)t0, live, x, b, bm, exact, m, s_key, xe);
+            const float gw = rt_weight<LW>(a, got, xe, m, sum);
+            if (live) {
+                mine = got;
+                w = gw;
             }
         }
-        if (lane < K) {
+        if (here && lane < K) {
             a.weights[t * K + lane] = w;
             a.experts_out[t * K + lane] = mine;
             s_pick[i * K + lane] = (int16_t)mine;
