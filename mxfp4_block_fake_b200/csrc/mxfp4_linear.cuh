@@ -274,33 +274,37 @@ __device__ __forceinline__ float act_of(float z)
 // 32 tokens of this thread's feature: v[i] = z of token i of `rows`. The
 // pointers are those of token 0 and this thread's column (the activated
 // width's where the activation is gated). Loads of the residual go ahead of
-// the stores eight tokens at a time, since y may be the residual.
-template <int ACT, bool F32, bool WHOLE>
+// the stores eight tokens at a time, since y may be the residual; without one,
+// four at a time keep the temporaries in registers (what spills goes to L2: the
+// stages leave the L1 cache next to nothing. 32768 x 4096 x 2048, swiglu, over 32
+// experts 193 against 176 us; with a residual 8192 x 4096 x 1024 94 / 116, and 73
+// once ln_prefetch asks for it ahead).
+template <int ACT, bool F32, bool WHOLE, bool RES>
 __device__ __forceinline__ void ln_finish32(const float (&v)[32], int rows, bool fok, char* y, int64_t ld_y,
                                             const char* res, int64_t ld_res)
 {
     constexpr int ESZ = F32 ? 4 : 2;
     constexpr bool GATED = ACT == MXFP4_ACT_SWIGLU;
-    constexpr int STEP = GATED ? 2 : 1;
+    constexpr int STEP = GATED ? 2 : 1, BATCH = RES ? 8 : 4;
     // gated: lanes 2j and 2j + 1 hold gate j and up j; of a pair of tokens the
     // even lane finishes the first, the odd lane the second
     const bool odd = GATED && (threadIdx.x & 1);
     const int first = odd ? 1 : 0;
     y += first * ld_y * ESZ;
-    if (res)
+    if constexpr (RES)
         res += first * ld_res * ESZ;
 #pragma unroll
-    for (int i0 = 0; i0 < 32; i0 += 8 * STEP) {
-        float o[8];
-        if (res) {
+    for (int i0 = 0; i0 < 32; i0 += BATCH * STEP) {
+        float o[BATCH];
+        if constexpr (RES) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+            for (int i = 0; i < BATCH; ++i) {
                 o[i] = WHOLE || (fok && i0 + STEP * i + first < rows) ? ln_load<F32>(res, 0) : 0.0f;
                 res += ld_res * (STEP * ESZ);
             }
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < BATCH; ++i) {
             float a;
             if constexpr (GATED) {
                 const int t = i0 + 2 * i;
@@ -310,10 +314,10 @@ __device__ __forceinline__ void ln_finish32(const float (&v)[32], int rows, bool
             } else {
                 a = act_of<ACT>(v[i0 + i]);
             }
-            o[i] = res ? a + o[i] : a;
+            o[i] = RES ? a + o[i] : a;
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < BATCH; ++i) {
             if (WHOLE || (fok && i0 + STEP * i + first < rows))
                 ln_store<F32>(y, 0, o[i]);
             y += ld_y * (STEP * ESZ);
@@ -321,7 +325,7 @@ __device__ __forceinline__ void ln_finish32(const float (&v)[32], int rows, bool
     }
 }
 
-template <bool F32, bool WHOLE>
+template <bool F32, bool WHOLE, bool RES>
 __device__ __forceinline__ void ln_epilogue32(const LnArgs& a, const float (&v)[32], int64_t row0, int rows, int f, bool fok)
 {
     constexpr int ESZ = F32 ? 4 : 2;
@@ -336,22 +340,35 @@ __device__ __forceinline__ void ln_epilogue32(const LnArgs& a, const float (&v)[
     }
     const int fo = a.act == MXFP4_ACT_SWIGLU ? f >> 1 : f;
     char* y = static_cast<char*>(a.y) + (row0 * a.ld_y + fo) * ESZ;
-    const char* res = a.residual ? static_cast<const char*>(a.residual) + (row0 * a.ld_res + fo) * ESZ : nullptr;
+    const char* res = RES ? static_cast<const char*>(a.residual) + (row0 * a.ld_res + fo) * ESZ : nullptr;
     // the branch is outside the loops: one activation's code runs
     switch (a.act) {
     case MXFP4_ACT_NONE:
-        return ln_finish32<MXFP4_ACT_NONE, F32, WHOLE>(v, rows, fok, y, a.ld_y, res, a.ld_res);
+        return ln_finish32<MXFP4_ACT_NONE, F32, WHOLE, RES>(v, rows, fok, y, a.ld_y, res, a.ld_res);
     case MXFP4_ACT_RELU:
-        return ln_finish32<MXFP4_ACT_RELU, F32, WHOLE>(v, rows, fok, y, a.ld_y, res, a.ld_res);
+        return ln_finish32<MXFP4_ACT_RELU, F32, WHOLE, RES>(v, rows, fok, y, a.ld_y, res, a.ld_res);
     case MXFP4_ACT_GELU:
-        return ln_finish32<MXFP4_ACT_GELU, F32, WHOLE>(v, rows, fok, y, a.ld_y, res, a.ld_res);
+        return ln_finish32<MXFP4_ACT_GELU, F32, WHOLE, RES>(v, rows, fok, y, a.ld_y, res, a.ld_res);
     case MXFP4_ACT_GELU_TANH:
-        return ln_finish32<MXFP4_ACT_GELU_TANH, F32, WHOLE>(v, rows, fok, y, a.ld_y, res, a.ld_res);
+        return ln_finish32<MXFP4_ACT_GELU_TANH, F32, WHOLE, RES>(v, rows, fok, y, a.ld_y, res, a.ld_res);
     case MXFP4_ACT_SILU:
-        return ln_finish32<MXFP4_ACT_SILU, F32, WHOLE>(v, rows, fok, y, a.ld_y, res, a.ld_res);
+        return ln_finish32<MXFP4_ACT_SILU, F32, WHOLE, RES>(v, rows, fok, y, a.ld_y, res, a.ld_res);
     default:
-        return ln_finish32<MXFP4_ACT_SWIGLU, F32, WHOLE>(v, rows, fok, y, a.ld_y, res, a.ld_res);
+        return ln_finish32<MXFP4_ACT_SWIGLU, F32, WHOLE, RES>(v, rows, fok, y, a.ld_y, res, a.ld_res);
     }
+}
+
+// Asks for a warp's part of the residual (32 features, TW tokens: a line each)
+// ahead of the product's end.
+template <bool F32, int TW>
+__device__ __forceinline__ void ln_prefetch(const LnArgs& a, int64_t row0, int rows, int f)
+{
+    if (f >= a.n)
+        return;
+    const int lane = threadIdx.x & 31, fo = (a.act == MXFP4_ACT_SWIGLU ? f >> 1 : f);
+    const int fw = __shfl_sync(__activemask(), fo, 0);
+    for (int t = lane; t < TW && t < rows; t += 32)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(a.residual) + ((row0 + t) * a.ld_res + fw) * (F32 ? 4 : 2)));
 }
 
 // True in one lane of the (converged) warp.
@@ -409,7 +426,7 @@ __device__ __forceinline__ void ln_stage(uint32_t d_tmem, uint32_t sf_col, uint3
     }
 }
 
-template <int FMT, int NT, bool F32>
+template <int FMT, int NT, bool F32, bool RES>
 __global__ void __launch_bounds__(LnSmem<FMT, NT>::THREADS, 1) linear_kernel(const __grid_constant__ LnMaps maps, const LnArgs a)
 {
     using F = LnFmt<FMT>;
@@ -581,6 +598,9 @@ __global__ void __launch_bounds__(LnSmem<FMT, NT>::THREADS, 1) linear_kernel(con
             const int f = tl.f0 + 128 * h + 32 * quad + lane;
             const bool fok = f < a.n;
             const float bias = a.bias && fok ? a.bias[(int64_t)tl.g * a.n + f] : 0.0f;
+            if (RES && h < tl.nh)
+                ln_prefetch<F32, TW>(a, tl.row0 + c0, tl.rows - c0, f);
+            __syncwarp();
             if (!__all_sync(FULL, ln_wait(smem_addr(&sm.acc_full[acc]), aph))) {
                 sm.err = 1;
                 break;
@@ -612,9 +632,9 @@ __global__ void __launch_bounds__(LnSmem<FMT, NT>::THREADS, 1) linear_kernel(con
                         break;
                     // whole chunks (every lane a feature, 32 tokens) take no predicates
                     if (rows >= 32 && __all_sync(FULL, fok))
-                        ln_epilogue32<F32, true>(a, v[0], tl.row0 + c0 + 32 * c, rows, f, fok);
+                        ln_epilogue32<F32, true, RES>(a, v[0], tl.row0 + c0 + 32 * c, rows, f, fok);
                     else
-                        ln_epilogue32<F32, false>(a, v[0], tl.row0 + c0 + 32 * c, rows, f, fok);
+                        ln_epilogue32<F32, false, RES>(a, v[0], tl.row0 + c0 + 32 * c, rows, f, fok);
                     // the next 32 tokens move up, so that the code exists once
 #pragma unroll
                     for (int d = 0; d + 1 < TW / 32; ++d)

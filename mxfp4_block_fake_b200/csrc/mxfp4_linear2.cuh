@@ -214,7 +214,7 @@ __device__ __forceinline__ void ln2_stage(uint32_t d_tmem, uint32_t sf_col, uint
     }
 }
 
-template <int FMT, bool F32>
+template <int FMT, bool F32, bool RES>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L2_THREADS, 1)
     linear2_kernel(const __grid_constant__ Ln2Maps maps, const LnArgs a)
 {
@@ -351,6 +351,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L2_THREADS, 1)
             const int f = tl.f0 + 128 * rank + 32 * quad + lane;
             const bool fok = f < a.n;
             const float bias = a.bias && fok ? a.bias[(int64_t)tl.g * a.n + f] : 0.0f;
+            if (RES && rank < tl.nh)
+                ln_prefetch<F32, 64>(a, tl.row0 + c0, tl.rows - c0, f);
+            __syncwarp();
             if (!__all_sync(FULL, ln_wait_cluster(smem_addr(&sm.acc_full), aph))) {
                 sm.err = 1;
                 break;
@@ -378,9 +381,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L2_THREADS, 1)
                     if (rows <= 0)
                         break;
                     if (rows >= 32 && __all_sync(FULL, fok))
-                        ln_epilogue32<F32, true>(a, v[0], tl.row0 + c0 + 32 * c, rows, f, fok);
+                        ln_epilogue32<F32, true, RES>(a, v[0], tl.row0 + c0 + 32 * c, rows, f, fok);
                     else
-                        ln_epilogue32<F32, false>(a, v[0], tl.row0 + c0 + 32 * c, rows, f, fok);
+                        ln_epilogue32<F32, false, RES>(a, v[0], tl.row0 + c0 + 32 * c, rows, f, fok);
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
                         v[0][i] = v[1][i];

@@ -382,7 +382,7 @@ template <int FMT, int NT, bool F32>
 static mxfp4_status launch_linear_t(const LnMaps& maps, const LnArgs& g, cudaStream_t s)
 {
     using SM = LnSmem<FMT, NT>;
-    const void* fn = (const void*)linear_kernel<FMT, NT, F32>;
+    const void* fn = g.residual ? (const void*)linear_kernel<FMT, NT, F32, true> : (const void*)linear_kernel<FMT, NT, F32, false>;
     const size_t smem = sizeof(SM) + 1024 + (size_t)(2 * (g.num_groups + 1)) * sizeof(int32_t);
     if (!allow_smem(fn, smem))
         return MXFP4_ECUDA;
@@ -464,7 +464,7 @@ static mxfp4_status launch_linear2(const mxfp4_linear_args* A, const LnMaps& map
         !encode_2d(&m2.sfx, CU_TENSOR_MAP_DATA_TYPE_UINT32, A->workspace, 128, (uint64_t)((g.m / L2_NT + g.num_groups) * ncb * 2), 512, 128,
                    2 * atoms, CU_TENSOR_MAP_SWIZZLE_NONE))
         return MXFP4_ECUDA;
-    const void* fn = (const void*)linear2_kernel<FMT, F32>;
+    const void* fn = g.residual ? (const void*)linear2_kernel<FMT, F32, true> : (const void*)linear2_kernel<FMT, F32, false>;
     const size_t plan = (size_t)(2 * (g.num_groups + 1)) * sizeof(int32_t), smem = sizeof(SM) + 1024 + plan;
     if (!allow_smem(fn, smem))
         return MXFP4_ECUDA;

@@ -90,23 +90,27 @@ __device__ __forceinline__ float rcp_approx(float v)
 template <int LW>
 __device__ __forceinline__ float part_max(float v)
 {
-    if constexpr (LW == 32)
+    if constexpr (LW == 32) {
         return warp_max(v);
+    } else {
 #pragma unroll
-    for (int o = LW / 2; o; o >>= 1)
-        v = max_nan(v, __shfl_xor_sync(FULL, v, o));
-    return v;
+        for (int o = LW / 2; o; o >>= 1)
+            v = max_nan(v, __shfl_xor_sync(FULL, v, o));
+        return v;
+    }
 }
 
 template <int LW>
 __device__ __forceinline__ uint32_t part_max(uint32_t v)
 {
-    if constexpr (LW == 32)
+    if constexpr (LW == 32) {
         return __reduce_max_sync(FULL, v);
+    } else {
 #pragma unroll
-    for (int o = LW / 2; o; o >>= 1)
-        v = max(v, __shfl_xor_sync(FULL, v, o));
-    return v;
+        for (int o = LW / 2; o; o >>= 1)
+            v = max(v, __shfl_xor_sync(FULL, v, o));
+        return v;
+    }
 }
 
 template <int LW>
