@@ -277,8 +277,7 @@ __device__ __forceinline__ float act_of(float z)
 // the stores eight tokens at a time, since y may be the residual; without one,
 // four at a time keep the temporaries in registers (what spills goes to L2: the
 // stages leave the L1 cache next to nothing. 32768 x 4096 x 2048, swiglu, over 32
-// experts 193 against 176 us; with a residual 8192 x 4096 x 1024 94 / 116, and 73
-// once ln_prefetch asks for it ahead).
+// experts 193 against 176 us; with a residual 8192 x 4096 x 1024 83 / 106).
 template <int ACT, bool F32, bool WHOLE, bool RES>
 __device__ __forceinline__ void ln_finish32(const float (&v)[32], int rows, bool fok, char* y, int64_t ld_y,
                                             const char* res, int64_t ld_res)
@@ -359,7 +358,10 @@ __device__ __forceinline__ void ln_epilogue32(const LnArgs& a, const float (&v)[
 }
 
 // Asks for a warp's part of the residual (32 features, TW tokens: a line each)
-// ahead of the product's end.
+// ahead of the product's end, where that is at most LN_SHORT stages away (k = 1024,
+// 4 stages: 69 against 83 us without; with 32 stages it came 3 % slower).
+constexpr int LN_SHORT = 16;
+
 template <bool F32, int TW>
 __device__ __forceinline__ void ln_prefetch(const LnArgs& a, int64_t row0, int rows, int f)
 {
@@ -598,7 +600,7 @@ __global__ void __launch_bounds__(LnSmem<FMT, NT>::THREADS, 1) linear_kernel(con
             const int f = tl.f0 + 128 * h + 32 * quad + lane;
             const bool fok = f < a.n;
             const float bias = a.bias && fok ? a.bias[(int64_t)tl.g * a.n + f] : 0.0f;
-            if (RES && h < tl.nh)
+            if (RES && nst <= LN_SHORT && h < tl.nh)
                 ln_prefetch<F32, TW>(a, tl.row0 + c0, tl.rows - c0, f);
             __syncwarp();
             if (!__all_sync(FULL, ln_wait(smem_addr(&sm.acc_full[acc]), aph))) {

@@ -351,7 +351,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L2_THREADS, 1)
             const int f = tl.f0 + 128 * rank + 32 * quad + lane;
             const bool fok = f < a.n;
             const float bias = a.bias && fok ? a.bias[(int64_t)tl.g * a.n + f] : 0.0f;
-            if (RES && rank < tl.nh)
+            if (RES && nst <= LN_SHORT && rank < tl.nh)
                 ln_prefetch<F32, 64>(a, tl.row0 + c0, tl.rows - c0, f);
             __syncwarp();
             if (!__all_sync(FULL, ln_wait_cluster(smem_addr(&sm.acc_full), aph))) {

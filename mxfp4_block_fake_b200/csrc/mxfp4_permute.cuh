@@ -193,6 +193,7 @@ __global__ void __launch_bounds__(NTHREADS) dispatch_stream_kernel(const Dispatc
     constexpr int NC = FMT == MXFP4_ELEM_E4M3 ? 8 : 4;  // code words of a block
     const uint32_t nblk = (uint32_t)(a.cols / 32), npad = (nblk + 3) & ~3u;
     constexpr int NW = 8 * ESZ;                         // words of a block
+    constexpr bool AHEAD = ESZ == 2;                    // fp32: 32 more registers would halve the resident warps
     const uint32_t total = (uint32_t)a.tokens * npad, stride = gridDim.x * NTHREADS;
     auto load = [&](uint32_t v, uint32_t (&w)[NW]) {
         const uint32_t t = v / npad, b = v - t * npad;
@@ -211,10 +212,12 @@ __global__ void __launch_bounds__(NTHREADS) dispatch_stream_kernel(const Dispatc
         const uint32_t t = u / npad, b = u - t * npad;
         const unsigned quad = 0xFu << (threadIdx.x & 28);
         const int32_t* rp = a.rows + (int64_t)t * a.k;
-        uint32_t wn[NW];
+        uint32_t wn[AHEAD ? NW : 1];
         const bool more = u + stride < total;
-        if (more)
-            load(u + stride, wn);  // the next block's loads are in flight while this one is worked on
+        if constexpr (AHEAD) {
+            if (more)
+                load(u + stride, wn);  // the next block's loads are in flight while this one is worked on
+        }
         uint32_t code[NC], e8 = 0;
         if (b < nblk) {
             if constexpr (ESZ == 2) {
@@ -286,10 +289,13 @@ __global__ void __launch_bounds__(NTHREADS) dispatch_stream_kernel(const Dispatc
         }
         if (a.ws_scales && (b & 3) == 0)
             a.ws_scales[u >> 2] = word;
-        if (more) {
+        if constexpr (AHEAD) {
+            if (more)
 #pragma unroll
-            for (int i = 0; i < NW; ++i)
-                w[i] = wn[i];
+                for (int i = 0; i < NW; ++i)
+                    w[i] = wn[i];
+        } else if (more) {
+            load(u + stride, w);
         }
     }
     if (!a.ws_scales)

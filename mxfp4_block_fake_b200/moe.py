@@ -186,6 +186,10 @@ class MXFP4MoE(nn.Module):
         self._laid_out = (moe_expert_operands(self.w1, **q)[:2], moe_expert_operands(self.w2, **q)[:2])
         return self
 
+    def _apply(self, fn, recurse=True):
+        self._laid_out = None  # moved or cast: the copy is of the old weights
+        return super()._apply(fn, recurse)
+
     @torch.no_grad()
     def update_balance(self, counts: torch.Tensor, rate: float = 1e-3) -> None:
         """Raises the balance of experts below the mean load, lowers the others'."""

@@ -904,6 +904,8 @@ def _linear_groups(a: _abi.LinearArgs, group_list, group_list_type: int, dev: to
     gl, ng = _group_args(group_list, group_list_type, dev)
     if gl.device != dev:
         raise ValueError(f"group_list must be a CUDA tensor on {dev}")
+    if ng < 1:
+        raise ValueError("group_list must name at least one group")
     a.group_list, a.num_groups, a.group_list_type = gl.data_ptr(), ng, int(group_list_type)
     return gl, ng
 

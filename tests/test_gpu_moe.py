@@ -660,6 +660,11 @@ def test_linear_refusals():
                 dict(out=ops.LinearResult(y=torch.zeros(50, 63, device="cuda").bfloat16()))):
         with pytest.raises((ValueError, TypeError)):
             ops.mxfp4_grouped_linear(a, sa, b, sb, **{**ok, **bad})
+    empty = torch.zeros(0, dtype=torch.int64, device="cuda")
+    with pytest.raises(ValueError):
+        ops.mxfp4_grouped_linear(a, sa, b, sb, empty, k=128)
+    with pytest.raises(ValueError):
+        ops.mxfp4_grouped_linear_bwd(rnd(50, 64).cuda(), rnd(50, 64).cuda(), empty)
     with pytest.raises(ValueError):
         ops.mxfp4_grouped_linear(a, sa[:100], b, sb, k=128)
     with pytest.raises(ValueError):

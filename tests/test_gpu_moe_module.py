@@ -65,6 +65,7 @@ def test_module_serves_what_it_trains(tokens):
     m.lay_out()
     with torch.no_grad():
         assert torch.equal(m(x, mask), out)
+    assert m.to("cuda")._laid_out is None      # moved: laid out again when asked
     m.update_balance(counts)
     low = counts.float() < counts.float().mean()
     assert bool((m.balance[low] > 0).all()) and bool((m.balance[~low] <= 0).all())
