@@ -462,7 +462,7 @@ mxfp4_status mxfp4_dual_level_qdq(const mxfp4_dual_level_args* args, mxfp4_strea
  *   bias        optional fp32 [experts]; token_mask optional [tokens] bytes.
  *   weights     fp32 [tokens][k]; chosen, rows int32 [tokens][k];
  *   slots       int32 [tokens * k]; counts int64 [experts].
- *   workspace   mxfp4_moe_route_workspace(tokens, experts) bytes, 4-byte
+ *   workspace   mxfp4_moe_route_workspace(tokens, experts) bytes, 16-byte
  *               aligned (may be NULL when that is 0); its contents matter
  *               to this call only.
  * Limits: experts <= 1024, k <= 32, num_groups <= 32, tokens * k < 2^31.

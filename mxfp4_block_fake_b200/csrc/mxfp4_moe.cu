@@ -141,7 +141,7 @@ static mxfp4_status run_route(const mxfp4_moe_route_args* A, cudaStream_t s)
         return MXFP4_EINVAL;
     const size_t esz = A->dtype == MXFP4_BF16 ? 2 : 4;
     if (!aligned(A->logits, esz) || !aligned(A->bias, 4) || !aligned(A->weights, 4) || !aligned(A->chosen, 4) ||
-        !aligned(A->rows, 4) || !aligned(A->slots, 4) || !aligned(A->counts, 8) || !aligned(A->workspace, 4))
+        !aligned(A->rows, 4) || !aligned(A->slots, 4) || !aligned(A->counts, 8) || !aligned(A->workspace, 16))
         return MXFP4_EINVAL;
     const int64_t need = mxfp4_moe_route_workspace(A->tokens, A->experts);
     if (need > 0 && (!A->workspace || A->workspace_bytes < need))

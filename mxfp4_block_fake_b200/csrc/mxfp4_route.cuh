@@ -746,24 +746,42 @@ __global__ void __launch_bounds__(RT_THREADS) route_place_kernel(const RouteArgs
     __shared__ int s_cnt[RT_MAX_EXPERTS], s_off[RT_MAX_EXPERTS], s_base[RT_MAX_EXPERTS];
     const int tid = threadIdx.x, E = a.experts, K = a.k;
     if constexpr (SCAN) {
-        // threads side by side on the chunks of one expert; integer sums, so their order does not matter
-        int segs = 1;
-        while (2 * segs * E <= RT_THREADS)
-            segs *= 2;
         for (int e = tid; e < E; e += RT_THREADS)
             s_cnt[e] = s_base[e] = 0;
         __syncthreads();
-        for (int i = tid; i < segs * E; i += RT_THREADS) {
-            const int seg = i / E, e = i - seg * E;
-            int before = 0, total = 0;
-#pragma unroll 8
+        // threads side by side on the chunks of four experts (whole 16-byte pieces
+        // where rows of counts are), integer sums, so their order does not matter
+        const int per = E % 4 == 0 ? 4 : 1, cols = E / per;
+        const int segs = max(1, RT_THREADS / cols);
+        for (int i = tid; i < segs * cols; i += RT_THREADS) {
+            const int seg = i / cols, e = (i - seg * cols) * per;
+            int before[4] = {0, 0, 0, 0}, total[4] = {0, 0, 0, 0};
+#pragma unroll 4
             for (int c = seg; c < a.chunks; c += segs) {
-                const int v = a.ws[(int64_t)c * E + e];
-                total += v;
-                before += c < (int)blockIdx.x ? v : 0;
+                const int* p = a.ws + (int64_t)c * E + e;
+                int v[4];
+                if (per == 4) {
+                    const int4 q = *reinterpret_cast<const int4*>(p);
+                    v[0] = q.x;
+                    v[1] = q.y;
+                    v[2] = q.z;
+                    v[3] = q.w;
+                } else {
+                    v[0] = *p;
+                    v[1] = v[2] = v[3] = 0;
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    total[q] += v[q];
+                    before[q] += c < (int)blockIdx.x ? v[q] : 0;
+                }
             }
-            atomicAdd(&s_cnt[e], total);
-            atomicAdd(&s_base[e], before);
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (q < per) {
+                    atomicAdd(&s_cnt[e + q], total[q]);
+                    atomicAdd(&s_base[e + q], before[q]);
+                }
         }
         __syncthreads();
         if (blockIdx.x == 0)
@@ -833,13 +851,12 @@ __global__ void __launch_bounds__(RT_THREADS) route_bwd_kernel(const RouteBwdArg
     const bool some = __any_sync(FULL, mine >= 0);
     float m = -INFINITY;
     bool bad = false;
-    if (some)
-        for (int e = lane; e < E; e += 32) {
-            const float x = rt_logit(a, t, e);
-            bad |= !(x < INFINITY);
-            m = fmaxf(m, x);
-        }
-    bad = __any_sync(FULL, bad);
+    for (int e = lane; e < E; e += 32) {  // read before it is known whether they count
+        const float x = rt_logit(a, t, e);
+        bad |= !(x < INFINITY);
+        m = fmaxf(m, x);
+    }
+    bad = __any_sync(FULL, bad) && some;
     m = warp_max(m);
     for (int e = lane; e < E; e += 32)
         s_d[e] = bad ? __uint_as_float(QNAN32) : 0.0f;

@@ -634,6 +634,43 @@ def test_linear_agrees_with_the_grouped_gemm():
     assert (one - two).norm() <= 2 * k * U32 * one.norm()
 
 
+def test_large_linear_captured_and_on_two_streams():
+    """The pair kernel and the decoding tiles at once on two streams, and the
+    former captured: the eager calls' bytes."""
+    n, k = 2304, 2048
+    big, small = [2048, 0, 2100], [1, 2, 0]
+    b, sb = zip(*(operand(n, k, "e2m1", 30 + e, 117, 119) for e in range(3)))
+    b, sb = torch.stack(b).cuda(), torch.cat(sb).cuda()
+    def call(sizes, seed, gl):
+        a, sa = operand(sum(sizes), k, "e2m1", seed)
+        a, sa = a.cuda(), sa.cuda()
+        return lambda: ops.mxfp4_grouped_linear(a, sa, b, sb, gl, k=k, group_list_type=1, activation="swiglu", check=False).y
+    lists = [torch.tensor(v, dtype=torch.int64, device="cuda") for v in (big, small)]
+    assert on_pairs("e2m1", sum(big), n, k, 3)
+    calls = [call(big, 1, lists[0]), call(small, 2, lists[1])]
+    g = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=side):
+        captured = calls[0]()
+    want = [c() for c in calls]
+    for _ in range(2):
+        captured.fill_(7.0)
+        g.replay()
+        assert torch.equal(captured, want[0])
+    streams = [torch.cuda.Stream() for _ in calls]
+    got = [[], []]
+    for _ in range(6):
+        for s, c, o in zip(streams, calls, got):
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                o.append(c())
+    torch.cuda.synchronize()
+    for o, w in zip(got, want):
+        assert all(torch.equal(v, w) for v in o)
+
+
 def test_linear_invalid_lists():
     a, sa = operand(50, 128, "e2m1", 1)
     b, sb = operand(128, 128, "e2m1", 2)
@@ -648,6 +685,17 @@ def test_linear_invalid_lists():
         assert int(r.status) == 1
         with pytest.raises(MXFP4ArgumentError):
             ops.mxfp4_grouped_linear_bwd(rnd(50, 64).cuda(), rnd(50, 64).cuda(), gl, group_list_type=kind)
+
+
+def test_invalid_lists_of_large_linears():
+    a, sa = operand(4096, 2048, "e2m1", 1)
+    b, sb = operand(4608, 2048, "e2m1", 2)
+    gl = torch.tensor([4000, 97], dtype=torch.int64, device="cuda")
+    y = torch.full((4096, 2304), 3.0, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(MXFP4ArgumentError):
+        ops.mxfp4_grouped_linear(a.cuda(), sa.cuda(), b.view(2, 2304, -1).cuda(), torch.cat([sb, sb])[: 2 * ops.scales_row_bytes(2304, 2048, 32, "mma")].cuda(),
+                                 gl, k=2048, group_list_type=1, out=ops.LinearResult(y=y))
+    assert bool((y == 3.0).all())
 
 
 def test_linear_refusals():
