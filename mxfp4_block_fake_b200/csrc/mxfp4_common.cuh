@@ -339,6 +339,13 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity)
 
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// Pairs of kernels on one stream, the second launched with the programmatic
+// serialisation attribute: the first lets it become resident once its own CTAs
+// are, and the second waits for the first's results (its writes included) before
+// it touches them or writes anything itself.
+__device__ __forceinline__ void let_dependents_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_prerequisite() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---------------------------------------------------------------------------
 // Row-wise bf16 block-32 quantisation core
 // ---------------------------------------------------------------------------

@@ -72,6 +72,7 @@ __global__ void __launch_bounds__(L2_NT) scale_tiles_kernel(const LnArgs a, uint
     __shared__ uint32_t s_word[SC_COLS][3 * 128];
     int32_t* s_tpre = sc_dyn;
     int32_t* s_rst = s_tpre + a.num_groups + 1;
+    let_dependents_start();
     const int64_t units = ln_plan<L2_NT>(a, s_tpre, s_rst);
     const int64_t nblk = a.k / 32, ncb = (nblk + 3) >> 2, row_atoms = (a.m + 127) >> 7;
     const int tid = threadIdx.x;
@@ -248,6 +249,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(L2_THREADS, 1)
         gm_fence_before();
     }
     const int64_t units = ln_plan<L2_NT>(a, s_tpre, s_rst);  // contains __syncthreads
+    wait_for_prerequisite();                                 // scale_tiles_kernel
     cluster_sync();                                          // the barriers of both CTAs are ready
     gm_fence_after();
     const uint32_t tmem = sm.tmem_base;

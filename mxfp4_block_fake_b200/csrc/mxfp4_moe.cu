@@ -66,6 +66,27 @@ static mxfp4_status launch1(const void* fn, int64_t grid, int threads, size_t sm
     return launched(cudaLaunchKernel(fn, dim3((unsigned)grid), dim3((unsigned)threads), args, smem, s));
 }
 
+// The second of a pair of kernels (wait_for_prerequisite): its launch and its start
+// overlap the first's end. The first must be the launch before it on the stream.
+static mxfp4_status launch_after(const void* fn, dim3 grid, int threads, size_t smem, void** args, cudaStream_t s)
+{
+    if (!allow_smem(fn, smem))
+        return MXFP4_ECUDA;
+    cudaLaunchAttribute at;
+    memset(&at, 0, sizeof(at));
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg;
+    memset(&cfg, 0, sizeof(cfg));
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return launched(cudaLaunchKernelExC(&cfg, fn, args));
+}
+
 // Grid of a grid-stride kernel over `units` threads' work.
 static int64_t stride_grid(const void* fn, int64_t units)
 {
@@ -176,13 +197,14 @@ static mxfp4_status run_route(const mxfp4_moe_route_args* A, cudaStream_t s)
     mxfp4_status e = launch1(fn, r.chunks, RT_THREADS, smem, r, s);
     if (e != MXFP4_OK || r.chunks == 1)
         return e;
+    void* args[] = {&r};
     // every CTA reading all chunks' counts costs chunks^2 * experts words: up to
     // 2^24 of them (about 3 us over the GPU) are cheaper than the scan's launch
     if ((int64_t)r.chunks * r.chunks * r.experts <= (int64_t)1 << 24)
-        return launch1((const void*)route_place_kernel<true>, r.chunks, RT_THREADS, 0, r, s);
-    e = launch1((const void*)route_scan_kernel, (r.experts + 31) / 32, 1024, 0, r, s);
+        return launch_after((const void*)route_place_kernel<true>, dim3((unsigned)r.chunks), RT_THREADS, 0, args, s);
+    e = launch_after((const void*)route_scan_kernel, dim3((unsigned)((r.experts + 31) / 32)), 1024, 0, args, s);
     if (e == MXFP4_OK)
-        e = launch1((const void*)route_place_kernel<false>, r.chunks, RT_THREADS, 0, r, s);
+        e = launch_after((const void*)route_place_kernel<false>, dim3((unsigned)r.chunks), RT_THREADS, 0, args, s);
     return e;
 }
 
@@ -301,7 +323,7 @@ static mxfp4_status run_dispatch(const mxfp4_moe_move_args* A, cudaStream_t s)
             DispatchArgs arg = a;
             void* args[] = {&arg};
             const dim3 grid((unsigned)((A->row_count + 127) / 128), (unsigned)((npad / 4 + SG_WORDS - 1) / SG_WORDS));
-            st = launched(cudaLaunchKernel((const void*)dispatch_scales_kernel, grid, dim3(NTHREADS), args, 0, s));
+            st = launch_after((const void*)dispatch_scales_kernel, grid, NTHREADS, 0, args, s);
         }
     }
     return st;
@@ -480,7 +502,7 @@ static mxfp4_status launch_linear2(const mxfp4_linear_args* A, const LnMaps& map
     if (st != MXFP4_OK)
         return st;
     void* args2[] = {&m2, &a};
-    return launched(cudaLaunchKernel(fn, dim3((unsigned)(2 * (bound < pairs ? bound : pairs))), dim3(L2_THREADS), args2, smem, s));
+    return launch_after(fn, dim3((unsigned)(2 * (bound < pairs ? bound : pairs))), L2_THREADS, smem, args2, s);
 }
 
 // Whether a product goes to pairs of SMs (given the workspace). Groups that fill
@@ -648,8 +670,7 @@ static mxfp4_status run_linear_bwd(const mxfp4_linear_args* A, cudaStream_t s)
     if (st == MXFP4_OK && A->grad_bias) {
         LnBwdArgs arg = b;
         void* args[] = {&arg};
-        st = launched(cudaLaunchKernel((const void*)linear_bias_kernel, dim3((unsigned)((A->n + NTHREADS - 1) / NTHREADS), (unsigned)groups),
-                                       dim3(NTHREADS), args, plan, s));
+        st = launch_after((const void*)linear_bias_kernel, dim3((unsigned)((A->n + NTHREADS - 1) / NTHREADS), (unsigned)groups), NTHREADS, plan, args, s);
     }
     return st;
 }

@@ -204,6 +204,7 @@ __global__ void __launch_bounds__(NTHREADS) dispatch_stream_kernel(const Dispatc
                 ld_nc_v8(xp + 32 * i, w + 8 * i);
         }
     };
+    let_dependents_start();
     uint32_t w[NW];
     uint32_t u = blockIdx.x * NTHREADS + threadIdx.x;
     if (u < total)
@@ -319,6 +320,7 @@ __global__ void __launch_bounds__(NTHREADS) dispatch_scales_kernel(const Dispatc
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t ncb = ((a.cols + 31) / 32 + 3) / 4, pairs = a.tokens * a.k;
     const int64_t row0 = (int64_t)blockIdx.x * 128, c0 = (int64_t)blockIdx.y * SG_WORDS;
+    wait_for_prerequisite();
     if (threadIdx.x < 128) {
         const int64_t r = row0 + threadIdx.x;
         int32_t t = -2;

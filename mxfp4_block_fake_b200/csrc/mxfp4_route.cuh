@@ -710,6 +710,7 @@ __global__ void __launch_bounds__(1024) route_scan_kernel(const RouteArgs a)
     const int e = blockIdx.x * 32 + lane;
     const int per = (a.chunks + 31) / 32;
     const int c0 = min(a.chunks, warp * per), c1 = min(a.chunks, c0 + per);
+    wait_for_prerequisite();
     int sum = 0;
     if (e < a.experts)
 #pragma unroll 8
@@ -745,6 +746,7 @@ __global__ void __launch_bounds__(RT_THREADS) route_place_kernel(const RouteArgs
 {
     __shared__ int s_cnt[RT_MAX_EXPERTS], s_off[RT_MAX_EXPERTS], s_base[RT_MAX_EXPERTS];
     const int tid = threadIdx.x, E = a.experts, K = a.k;
+    wait_for_prerequisite();
     if constexpr (SCAN) {
         for (int e = tid; e < E; e += RT_THREADS)
             s_cnt[e] = s_base[e] = 0;
