@@ -508,16 +508,16 @@ static mxfp4_status launch_linear2(const mxfp4_linear_args* A, const LnMaps& map
 // Whether a product goes to pairs of SMs (given the workspace). Groups that fill
 // 256-token tiles on average; tiles for most of the device (1024 x 4096 x 4096 31
 // against the single-SM kernel's 24 us, 4096 x 4096 x 4096 57 / 63); and eight
-// stages along K per bf16 stream of results and residuals: its one accumulator
-// does not hide a long epilogue (32768 x 4096 over 32 experts, E2M1, bf16 results:
-// k = 1024 184 / 160 us, 2048 194 / 194, 2560 203 / 226, 7168 391 / 486; E4M3 2049 x
-// 14336 x 4096, 32 stages: bf16 results 127 / 135, three fp32 streams 235 / 191).
+// stages along K, since its one accumulator waits for both CTAs' epilogues
+// (32768 x 4096 over 32 experts, E2M1, bf16 results: k = 1024 184 / 160 us, 2048 194 /
+// 194, 2560 203 / 226, 7168 391 / 486; with a residual, k = 2048, 248 / 240; three fp32
+// streams: E2M1 16384 rows, k = 2048 250 / 250, 4096 275 / 284, E4M3 2049 x 14336 x
+// 4096 182 / 197).
 static bool linear_on_pairs(const mxfp4_linear_args* A)
 {
     const int64_t stage = A->elem_format == MXFP4_ELEM_E2M1 ? LnFmt<MXFP4_ELEM_E2M1>::BK : LnFmt<MXFP4_ELEM_E4M3>::BK;
     const int64_t groups = A->group_list ? A->num_groups : 1;
-    const int64_t streams = (1 + (A->preact != nullptr) + (A->residual != nullptr)) * (A->d_dtype == MXFP4_F32 ? 2 : 1);
-    return A->m / groups >= L2_NT && A->k >= 8 * stage * streams && (A->m / L2_NT) * (A->n / LN_FT) >= 128 &&
+    return A->m / groups >= L2_NT && A->k >= 8 * stage && (A->m / L2_NT) * (A->n / LN_FT) >= 128 &&
            groups <= Ln2Smem<MXFP4_ELEM_E2M1>::MAX_GROUPS && scale_tiles_bytes(A->m, A->k, groups) / 512 <= INT32_MAX &&
            groups * (mxfp4_scales_row_bytes(A->n, A->k, 32, MXFP4_SCALES_MMA) >> 9) <= INT32_MAX &&  // 32-bit coordinates
            aligned(A->a_scales, 16);

@@ -447,7 +447,7 @@ __device__ __forceinline__ int rt_select(const RouteArgs& a, int t, bool live, c
         // equal keys: the lowest lane holds the lowest expert
         const uint32_t head = v[0] & ~INDEX, top = part_max<LW>(head);
         const bool some = top > CLOSED;
-        if (!__any_sync(FULL, some))
+        if (LW == 32 ? !some : !__any_sync(FULL, some))
             break;
         const int at = __ffs(part_ballot<LW>(some && head == top)) - 1;  // -1: nothing is left to this token
         const uint32_t taken = __shfl_sync(FULL, v[0], at & (LW - 1), LW);

@@ -22,6 +22,15 @@ from . import ops
 from .qat import SCALE_FACTOR, _Spec
 
 
+def _not_captured(what: str) -> None:
+    """The backwards here are refused under stream capture: the experts'
+    products copy counts to the host, and autograd's own joining of a leaf's
+    eager stream with a capturing one ends the process. Forwards can be
+    captured, and so can the ops' own backward calls."""
+    if torch.cuda.is_current_stream_capturing():
+        raise RuntimeError(f"the backward of {what} cannot be captured into a CUDA graph; call the ops entry points instead")
+
+
 class _Route(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, k, kw):
@@ -34,6 +43,7 @@ class _Route(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, grad, *_):
+        _not_captured("moe_route")
         logits, experts = ctx.saved_tensors
         return ops.mxfp4_moe_route_bwd(grad, logits, experts, **ctx.rule), None, None
 
@@ -53,6 +63,7 @@ class _Dispatch(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, grad):
+        _not_captured("moe_dispatch")
         (rows,) = ctx.saved_tensors
         return ops.mxfp4_moe_combine(grad, rows), None
 
@@ -73,6 +84,7 @@ class _Combine(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, grad):
+        _not_captured("moe_combine")
         y, rows, weights = ctx.saved_tensors
         need_y, _, need_w, _ = ctx.needs_input_grad
         gy = gw = None
@@ -124,8 +136,7 @@ class _GroupedLinear(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, grad):
-        if torch.cuda.is_current_stream_capturing():
-            raise RuntimeError("the backward of moe_grouped_linear copies counts to the host and cannot be captured")
+        _not_captured("moe_grouped_linear")
         xq, wq, preact, counts = ctx.saved_tensors
         gz, gb = ops.mxfp4_grouped_linear_bwd(grad, preact, counts, group_list_type=1, activation=ctx.activation,
                                               bias_grad=ctx.has_bias, check=False, out=torch.zeros_like(preact))

@@ -541,12 +541,10 @@ def test_linear_epilogue(act, out, everything, fmt):
     linear_case([20, 0, 150, 3], 180, 262, 256, fmt, act=act, out=out, bias=everything, residual=everything, preact=everything)
 
 
-def on_pairs(fmt, m, n, k, groups, streams=1):
+def on_pairs(fmt, m, n, k, groups):
     a = ops._abi.LinearArgs()
     a.elem_format, a.m, a.n, a.k, a.d_dtype = ops._elem_format(fmt), m, n, k, ops._abi.BF16
     a.group_list, a.num_groups = 4096, groups        # not followed
-    a.preact = 4096 if streams > 1 else None
-    a.residual = 4096 if streams > 2 else None
     return ops._abi.mxfp4_grouped_linear_fwd_workspace(a) > 0
 
 
@@ -566,9 +564,9 @@ def test_linear_of_large_groups(fmt, sizes, m, n, k):
 @pytest.mark.parametrize("out", ["bf16", "fp32"])
 @pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
 def test_linear_epilogue_of_large_groups(act, out, fmt):
-    k = 2048 * 3 if fmt == "e2m1" else 1024 * 3 + 32
-    assert on_pairs(fmt, 4096, 2310, k, 3, streams=3)
-    linear_case([1300, 0, 2470], 4096, 2310, k * (2 if out == "fp32" else 1), fmt, act=act, out=out, bias=True, residual=True, preact=True, list_type=0)
+    k = 2048 if fmt == "e2m1" else 1056
+    assert on_pairs(fmt, 4096, 2310, k, 3)
+    linear_case([1300, 0, 2470], 4096, 2310, k, fmt, act=act, out=out, bias=True, residual=True, preact=True, list_type=0)
 
 
 def test_linear_with_and_without_its_workspace():

@@ -97,6 +97,32 @@ def test_module_in_a_graph():
         assert torch.equal(out, w)
 
 
+@pytest.mark.parametrize("which", ["route", "dispatch", "combine"])
+def test_captured_backwards_are_refused(which):
+    """While an eager graph of the same leaves lives: an exception, and the process and the stream go on."""
+    x = rnd(20, 64, seed=1).requires_grad_(True)
+    lg = rnd(20, 4, seed=2).requires_grad_(True)
+
+    def forward():
+        r = moe.moe_route(lg, 2)
+        d = moe.moe_dispatch(x, r)
+        return {"route": r.weights, "dispatch": d, "combine": moe.moe_combine(d, r)}[which].square().sum()
+
+    alive = forward()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        forward()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    with pytest.raises(RuntimeError, match="captured"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph()):
+            forward().backward()
+    alive.backward()
+    torch.cuda.synchronize()
+    assert bool(torch.isfinite((lg if which == "route" else x).grad).all())
+
+
 def test_optimiser_steps_run():
     torch.manual_seed(2)
     m = MXFP4MoE(64, 64, 4, 2, device="cuda", dtype=torch.float32)
