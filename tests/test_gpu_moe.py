@@ -783,6 +783,57 @@ def test_linear_backward_strided():
     assert bool(((one[1] - two[1]).abs() <= 2 * 69 * U32 * one[0].abs().sum(0)).all())
 
 
+# ------------------------------------------------------------------- offsets past 32 bits
+
+def test_rows_past_32_bits():
+    """2.3e9 elements of expert rows: the last ones as right as the first."""
+    t, k, cols = 40000, 8, 7168
+    x = torch.randn(t, cols, device="cuda").bfloat16()
+    rows = torch.randperm(t * k, device="cuda").int().view(t, k)
+    d = ops.mxfp4_moe_dispatch(x, rows, emit_codes=True, elem_format="e4m3", scale_mode="floor")
+    q = ops.mxfp4_qdq_fwd(x, emit_values=False, emit_codes=True, elem_format="e4m3", scale_mode="floor")
+    for i in (0, 1, t // 2, t - 2, t - 1):
+        for j in (0, k - 1):
+            r = int(rows[i, j])
+            assert torch.equal(d.values[r], x[i]) and torch.equal(d.codes[r], q.codes_row[i])
+    high = (rows.long() * cols > 2 ** 31).any(1).nonzero()[-3:, 0].tolist()
+    assert high
+    for i in high:
+        for j in range(k):
+            assert torch.equal(d.values[int(rows[i, j])], x[i]) and torch.equal(d.codes[int(rows[i, j])], q.codes_row[i])
+    out = ops.mxfp4_moe_combine(d.values, rows)
+    assert torch.equal(out, k * x)                 # eight equal values: exact
+    del d, q
+    gy, gw = ops.mxfp4_moe_combine_bwd(x, out[:1].expand(t * k, cols), rows, grad_weights=False)
+    for i in high:
+        assert torch.equal(gy[int(rows[i, 0])], x[i])
+
+
+def test_results_past_32_bits():
+    """2.4e9 results of a product; rows of a slice by themselves give the same bytes."""
+    m, n, k = 300032, 8192, 64
+    a, sa = operand(m, k, "e2m1", 3)
+    b, sb = operand(n, k, "e2m1", 4)
+    a, sa, b, sb = a.cuda(), sa.cuda(), b.cuda(), sb.cuda()
+    y = ops.mxfp4_grouped_linear(a, sa, b, sb, k=k).y
+    for first in (0, 256 * 1024, m - 256):
+        part = ops.mxfp4_grouped_linear(a[first:first + 256], sa[first * 4:(first + 256) * 4], b, sb, k=k).y
+        assert torch.equal(y[first:first + 256], part)
+
+
+def test_logits_past_32_bits():
+    t, e = 2100000, 1024
+    x = torch.randn(t, e, device="cuda", dtype=torch.bfloat16)
+    r = ops.mxfp4_moe_route(x, 2)
+    one = ops.mxfp4_moe_route(x[-100:], 2)
+    assert torch.equal(r.experts[-100:], one.experts) and torch.equal(r.weights[-100:], one.weights)
+    assert int(r.counts.sum()) == 2 * t
+    last = r.slots[r.rows[-1].long()]
+    assert last.tolist() == [2 * t - 2, 2 * t - 1]
+    g = ops.mxfp4_moe_route_bwd(torch.ones(t, 2, device="cuda"), x, r.experts, renormalize=False)
+    assert torch.equal(g[-100:], ops.mxfp4_moe_route_bwd(torch.ones(100, 2, device="cuda"), x[-100:], one.experts, renormalize=False))
+
+
 # ------------------------------------------------------------------ as they are used together
 
 def layer(x, router, w1, s1, w2, s2, hidden, k, mask=None, check=False):
