@@ -112,6 +112,10 @@ def moe_expert_operands(weight: torch.Tensor, scale_factor: float = SCALE_FACTOR
     """Expert weights [E, n, k] as the operand of mxfp4_grouped_linear: codes
     [E, n, k / 2], E scale buffers, and (values) the values they stand for."""
     spec = _Spec.of(32, scale_factor, scale_mode)
+    e, n, k = weight.shape
+    if n % 128 == 0 and weight.is_contiguous():  # whole scale atoms: the experts' buffers are those of one matrix
+        q = _operand(spec, weight.detach().view(e * n, k), values)
+        return q.codes_row.view(e, n, -1), q.scales_row.view(e, -1), q.y_row.view(e, n, k) if values else None
     parts = [_operand(spec, w, values) for w in weight.detach()]
     codes = torch.stack([p.codes_row for p in parts])
     scales = torch.stack([p.scales_row for p in parts])
@@ -120,7 +124,7 @@ def moe_expert_operands(weight: torch.Tensor, scale_factor: float = SCALE_FACTOR
 
 class _GroupedLinear(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, weight, bias, counts, activation, scale_factor, scale_mode):
+    def forward(ctx, x, weight, bias, counts, activation, scale_factor, scale_mode, check):
         spec = _Spec.of(32, scale_factor, scale_mode)
         xq = _operand(spec, x, True)
         codes, scales, wq = moe_expert_operands(weight, scale_factor, scale_mode, values=True)
@@ -128,7 +132,7 @@ class _GroupedLinear(torch.autograd.Function):
         zeros = lambda cols: torch.zeros((m, cols), dtype=x.dtype, device=x.device)  # noqa: E731 (rows of no expert)
         out = ops.LinearResult(y=zeros(n // 2 if activation == "swiglu" else n), preact=zeros(n))
         r = ops.mxfp4_grouped_linear(xq.codes_row, xq.scales_row, codes, scales, counts, k=x.shape[1], group_list_type=1,
-                                     bias=bias, activation=activation, out_dtype=x.dtype, out=out, check=False)
+                                     bias=bias, activation=activation, out_dtype=x.dtype, out=out, check=check)
         ctx.save_for_backward(xq.y_row, wq, r.preact, counts)
         ctx.activation, ctx.has_bias = activation, bias is not None
         return r.y
@@ -148,18 +152,21 @@ class _GroupedLinear(torch.autograd.Function):
                 torch.mm(gz[rows], wq[e], out=gx[rows])
                 torch.mm(gz[rows].t(), xq[rows], out=gw[e])
             first += size
-        return gx, gw, gb, None, None, None, None
+        return gx, gw, gb, None, None, None, None, None
 
 
 def moe_grouped_linear(x: torch.Tensor, weight: torch.Tensor, counts: torch.Tensor, bias: torch.Tensor | None = None,
-                       activation: str = "none", scale_factor: float = SCALE_FACTOR, scale_mode: str = "page") -> torch.Tensor:
+                       activation: str = "none", scale_factor: float = SCALE_FACTOR, scale_mode: str = "page",
+                       check: bool = True) -> torch.Tensor:
     """act(Q(x_e) Q(W_e)^T + b_e) for the rows that counts gives to each expert
     (x in expert order; rows behind them give zero). weight [E, n, k], k a
     multiple of 64; bias float32 [E, n]; activation as in
-    ops.mxfp4_grouped_linear. The backward copies counts to the host."""
+    ops.mxfp4_grouped_linear. check synchronises and raises for counts that are
+    negative or exceed the rows (without it such counts give zeros); counts of
+    moe_route need none. The backward copies counts to the host."""
     if weight.ndim != 3 or x.ndim != 2 or weight.shape[2] != x.shape[1] or weight.dtype != x.dtype:
         raise ValueError("x must be [rows, k] and weight [experts, n, k], of one dtype")
-    return _GroupedLinear.apply(x, weight, bias, counts, activation, scale_factor, scale_mode)
+    return _GroupedLinear.apply(x, weight, bias, counts, activation, scale_factor, scale_mode, bool(check))
 
 
 class MXFP4MoE(nn.Module):
@@ -172,8 +179,9 @@ class MXFP4MoE(nn.Module):
     scores for the choice only; update_balance moves it against the load.
 
     With gradients enabled the forward quantises the weights each call. For
-    serving, lay_out() quantises them once; until it is called again, forwards
-    without gradients use that copy."""
+    serving, lay_out() quantises them once, and forwards without gradients use
+    that copy until a weight is changed, replaced or moved (in-place changes as
+    autograd counts them; call it again after others, such as through .data)."""
 
     def __init__(self, cols: int, hidden: int, experts: int, k: int, *, score: str = "softmax", num_groups: int = 1,
                  topk_groups: int | None = None, renormalize: bool = True, scale: float = 1.0, balance: bool = False,
@@ -194,8 +202,15 @@ class MXFP4MoE(nn.Module):
     def lay_out(self) -> "MXFP4MoE":
         """Quantises the experts' weights for serving."""
         q = dict(scale_factor=self.scale_factor, scale_mode=self.scale_mode)
-        self._laid_out = (moe_expert_operands(self.w1, **q)[:2], moe_expert_operands(self.w2, **q)[:2])
+        self._laid_out = (moe_expert_operands(self.w1, **q)[:2], moe_expert_operands(self.w2, **q)[:2], self._weights())
         return self
+
+    def _weights(self):
+        """The experts' weights with their counts of in-place changes."""
+        return [(w, -1 if w.is_inference() else w._version) for w in (self.w1, self.w2)]
+
+    def _copy_is_current(self) -> bool:
+        return self._laid_out is not None and all(a is b and i == j for (a, i), (b, j) in zip(self._laid_out[2], self._weights()))
 
     def _apply(self, fn, recurse=True):
         self._laid_out = None  # moved or cast: the copy is of the old weights
@@ -216,11 +231,11 @@ class MXFP4MoE(nn.Module):
         mask = None if token_mask is None else token_mask.reshape(-1)
         r = moe_route(logits, self.k, bias=self.balance, token_mask=mask, **self.rule)
         q = dict(scale_factor=self.scale_factor, scale_mode=self.scale_mode)
-        if torch.is_grad_enabled() or self._laid_out is None:
-            h = moe_grouped_linear(moe_dispatch(x2, r), self.w1, r.counts, activation="swiglu", **q)
-            y = moe_grouped_linear(h, self.w2, r.counts, **q)
+        if torch.is_grad_enabled() or not self._copy_is_current():
+            h = moe_grouped_linear(moe_dispatch(x2, r), self.w1, r.counts, activation="swiglu", check=False, **q)
+            y = moe_grouped_linear(h, self.w2, r.counts, check=False, **q)
         else:
-            (c1, s1), (c2, s2) = self._laid_out
+            (c1, s1), (c2, s2), _ = self._laid_out
             d = ops.mxfp4_moe_dispatch(x2, r.rows, emit_values=False, emit_codes=True, **q)
             h = ops.mxfp4_grouped_linear(d.codes, d.scales, c1, s1, r.counts, k=x2.shape[1], group_list_type=1,
                                          activation="swiglu", out_dtype=x2.dtype, check=False).y

@@ -6,7 +6,7 @@ from __future__ import annotations
 import pytest
 import torch
 
-from mxfp4_block_fake_b200 import MXFP4MoE, moe, mxfp4_quant_dequant, ops
+from mxfp4_block_fake_b200 import MXFP4ArgumentError, MXFP4MoE, moe, mxfp4_quant_dequant, ops
 from tests import moe_ref as R
 
 pytestmark = pytest.mark.gpu
@@ -121,6 +121,49 @@ def test_captured_backwards_are_refused(which):
     alive.backward()
     torch.cuda.synchronize()
     assert bool(torch.isfinite((lg if which == "route" else x).grad).all())
+
+
+@pytest.mark.parametrize("change", ["step", "load", "replace"])
+def test_laid_out_copy_is_not_used_for_changed_weights(change):
+    torch.manual_seed(3)
+    m, other = (MXFP4MoE(64, 128, 4, 2, device="cuda") for _ in range(2))
+    x = rnd(30, 64, seed=3, dtype=torch.bfloat16)
+    m.lay_out()
+    with torch.no_grad():
+        old = m(x)
+        if change == "step":
+            for p, q in zip(m.parameters(), other.parameters()):
+                p.add_(q)
+        elif change == "load":
+            m.load_state_dict(other.state_dict())
+        else:
+            m.router, m.w1, m.w2 = other.router, other.w1, other.w2
+        got = m(x)
+        assert not torch.equal(got, old)
+        assert torch.equal(m.lay_out()(x), got)
+        if change != "step":
+            assert torch.equal(other(x), got)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("scale_mode", ["page", "floor"])
+def test_expert_operands(dtype, scale_mode):
+    """Whole scale atoms, ragged ones and transposed storage: expert by expert."""
+    for w in (rnd(3, 256, 96, seed=4, dtype=dtype), rnd(3, 72, 64, seed=5, dtype=dtype),
+              rnd(3, 64, 128, seed=6, dtype=dtype).transpose(1, 2)):
+        codes, scales, values = moe.moe_expert_operands(w, scale_mode=scale_mode, values=True)
+        for e in range(3):
+            q = ops.mxfp4_qdq_fwd(w[e], block=32, scale_mode=scale_mode, emit_codes=True, scales_layout="mma")
+            assert torch.equal(codes[e], q.codes_row) and torch.equal(scales[e], q.scales_row) and torch.equal(values[e], q.y_row)
+
+
+@pytest.mark.parametrize("counts", [[3, 4], [-1, 2], [7, 0]])
+def test_counts_that_do_not_fit(counts):
+    x, w = rnd(6, 64, seed=7), rnd(2, 8, 64, seed=8)
+    c = torch.tensor(counts).cuda()
+    with pytest.raises(MXFP4ArgumentError):
+        moe.moe_grouped_linear(x, w, c)
+    assert not moe.moe_grouped_linear(x, w, c, check=False).any()
 
 
 def test_optimiser_steps_run():
