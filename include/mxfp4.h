@@ -443,7 +443,8 @@ mxfp4_status mxfp4_dual_level_qdq(const mxfp4_dual_level_args* args, mxfp4_strea
  * Routing. Per token with logits x_0 .. x_{E-1} (fp32 or bf16):
  *   score   s_e = softmax(x)_e or 1 / (1 + exp(-x_e))
  *   key     s_e + bias_e (bias NULL: s_e), compared in 64 bits (with no bias,
- *           or one value for all experts, by x_e itself, which orders alike);
+ *           or one value for all experts, by x_e itself, which orders alike;
+ *           zeros of both signs are equal);
  *           an expert is closed to the token when x_e is -inf or bias_e is not
  *           finite
  *   groups  with num_groups > 1 the experts form num_groups runs of E /

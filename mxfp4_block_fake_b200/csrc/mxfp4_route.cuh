@@ -339,7 +339,7 @@ __device__ __forceinline__ int rt_select(const RouteArgs& a, int t, bool live, c
     if (exact && !(a.groups > 1 && a.top2)) {
 #pragma unroll
         for (int i = 0; i < NV; ++i)
-            key[i] = b[i] > -INFINITY ? x[i] : -INFINITY;
+            key[i] = b[i] > -INFINITY ? x[i] + 0.0f : -INFINITY;  // (-0 becomes +0: equal logits are equal words)
     } else {
         if constexpr (!SIG) {
             float total = 0.0f;
@@ -423,7 +423,7 @@ __device__ __forceinline__ int rt_select(const RouteArgs& a, int t, bool live, c
         if (exact)  // the scores were for the groups' ranks
 #pragma unroll
             for (int i = 0; i < NV; ++i)
-                key[i] = b[i] > -INFINITY ? x[i] : -INFINITY;
+                key[i] = b[i] > -INFINITY ? x[i] + 0.0f : -INFINITY;
     }
     // words at or below that of -inf are closed
     constexpr uint32_t CLOSED = 0x007FFFFFu;
@@ -463,7 +463,7 @@ __device__ __forceinline__ int rt_select(const RouteArgs& a, int t, bool live, c
         }
     }
     const int e = word ? src * NV + (int)(INDEX - (word & INDEX)) : -1;
-    // bf16 logits are whole in their words: nothing to check
+    // bf16 logits are whole in their words, zeros of both signs as one: nothing to check
     xe = e >= 0 ? rt_logit<BF16>(a, t, e) : -INFINITY;
     if (!(exact && BF16)) {
         const float be = e >= 0 && a.bias ? a.bias[e] : 0.0f;

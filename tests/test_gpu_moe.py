@@ -253,6 +253,29 @@ def test_route_backward_special_rows():
     assert bool((got[5] == 0).all())
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("constant_bias", [False, True])
+@pytest.mark.parametrize("experts,groups", [(24, 1), (64, 4), (256, 1), (256, 8), (1000, 10)])
+@pytest.mark.parametrize("k", [1, 5])
+def test_route_zeros_of_both_signs(dtype, constant_bias, experts, groups, k):
+    """+0.0 and -0.0 are equal logits: the lower expert comes first, inside the
+    choice, at its end, and between lanes."""
+    g = gen(experts + k)
+    x = -torch.rand(160, experts, generator=g).to(DT[dtype]) - 1.0
+    share = torch.linspace(0.0, 1.0, 160)[:, None] ** 3
+    zero = torch.rand(160, experts, generator=g) < share
+    sign = torch.rand(160, experts, generator=g) < 0.5
+    x = torch.where(zero, torch.where(sign, -0.0, 0.0).to(x.dtype), x)
+    x[0] = -1.0
+    x[0, 3], x[0, 20] = -0.0, 0.0
+    x[1] = -0.0
+    x[1, -1] = 0.0
+    bias = torch.full((experts,), 0.25) if constant_bias else None
+    for score in ("softmax", "sigmoid"):
+        check_route(x, k, score=score, bias=bias, num_groups=groups, topk_groups=max(1, groups // 2))
+        check_route(x, k, score=score, bias=bias, num_groups=groups, topk_groups=max(1, groups // 2), group_score="max")
+
+
 # ------------------------------------------------------------------ dispatch and combine
 
 def a_plan(tokens, experts, k, seed=0, masked=0.0):
