@@ -417,7 +417,7 @@ __device__ __forceinline__ int rt_select(const RouteArgs& a, int t, bool live, c
             // two keys, whose scores are at most 1 and sum to |rank| + 2 bm
             const float low = -part_max<LW>(keep ? -rank : -INFINITY), high = part_max<LW>(keep ? -INFINITY : rank);
             const float size = fmaxf(fabsf(low), fabsf(high)) + 2.0f * bm;
-            const float err = fminf(size, 2.0f) * (SIG ? 0x1p-19f : 0x1p-17f) + size * 0x1p-22f + 0x1p-24f;
+            const float err = fminf(size, 2.0f) * (SIG ? 0x1.4p-19f : 0x1p-17f) + size * 0x1p-22f + 0x1p-24f;
             unsure = high > -INFINITY && low - high <= 2.0f * err;
         }
         if (exact)  // the scores were for the groups' ranks
@@ -474,11 +474,14 @@ __device__ __forceinline__ int rt_select(const RouteArgs& a, int t, bool live, c
         if (exact) {
             close = lane < K - 1 ? !(xe > xn || (xe == xn && e < en)) : ((word ^ wn) & ~INDEX) == 0u;
         } else {
-            // the whole keys again; behind the last choice nothing exceeds the
-            // next word with its low bits full
+            // the whole keys again; behind the last choice no key exceeds the next
+            // word with its low bits full, but any expert may hold such a key: its
+            // score is the key less its bias, and at most the row's largest
             const float se = rt_score<SIG>(xe, m, r), sn = rt_score<SIG>(xn, m, r), ke = se + be, kn = sn + bn;
-            const float bound = lane < K - 1 ? kn : rt_unorder(wn | INDEX);
-            close = ke - bound <= rt_key_error<SIG>(se, ke) + rt_key_error<SIG>(sn, kn);
+            const bool last = lane == K - 1;
+            const float bound = last ? rt_unorder(wn | INDEX) : kn;
+            const float rest = fminf(bound + bm, SIG ? 1.0f : r) * (SIG ? 0x1.4p-19f : 0x1p-17f) + fabsf(bound) * 0x1p-23f + 0x1p-25f;
+            close = !(ke - bound > rt_key_error<SIG>(se, ke) + (last ? rest : rt_key_error<SIG>(sn, kn)));
             if (lane < K - 1 && xe == xn && be == bn)
                 close = e > en;  // equal keys: the lower expert first
         }

@@ -276,6 +276,36 @@ def test_route_zeros_of_both_signs(dtype, constant_bias, experts, groups, k):
         check_route(x, k, score=score, bias=bias, num_groups=groups, topk_groups=max(1, groups // 2), group_score="max")
 
 
+@pytest.mark.parametrize("experts", [64, 256])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("p", [0.942, 0.76, 0.6])
+def test_route_key_left_out_with_a_large_score(experts, score, p):
+    """An expert whose large score its bias takes back to a key near 0 (so its
+    key's error is that of the score), against a last choice of a small score, with
+    a third expert of a small score and key between the two in fp32."""
+    high, fill, third, last = 5, 6, 7, experts - 3
+    one = math.log(p / (1 - p))
+    step = 2.0 ** (math.floor(math.log2(one)) - 23)
+    at = one + step * torch.arange(-90, 91, dtype=torch.float64)
+    small = torch.logspace(-7.4, -6.4, 33, dtype=torch.float64)
+    x = torch.full((at.numel(), small.numel(), experts), -60.0, dtype=torch.float64)
+    x[:, :, high] = at[:, None]
+    # softmax: the fill's logit 0 and the high one's make p; sigmoid: each by itself
+    x[:, :, fill] = 0.0
+    total = math.log(1 / (1 - p)) if score == "softmax" else 0.0
+    x[:, :, last] = small.log()[None, :] + total
+    x[:, :, third] = math.log(1e-9) + total
+    x = x.view(-1, experts).float()
+    bias = torch.zeros(experts)
+    bias[high], bias[fill] = -p, -2.0
+    v = x.cuda().double()
+    key = (torch.sigmoid(v) if score == "sigmoid" else torch.softmax(v, 1)) + bias.cuda().double()
+    for k in (1, 2):
+        want = key.sort(dim=1, descending=True, stable=True).indices[:, :k]
+        r = ops.mxfp4_moe_route(x.cuda(), k, score=score, bias=bias.cuda())
+        assert torch.equal(r.experts.long(), want)
+
+
 # ------------------------------------------------------------------ dispatch and combine
 
 def a_plan(tokens, experts, k, seed=0, masked=0.0):
