@@ -418,7 +418,7 @@ __device__ __forceinline__ int rt_select(const RouteArgs& a, int t, bool live, c
             const float low = -part_max<LW>(keep ? -rank : -INFINITY), high = part_max<LW>(keep ? -INFINITY : rank);
             const float size = fmaxf(fabsf(low), fabsf(high)) + 2.0f * bm;
             const float err = fminf(size, 2.0f) * (SIG ? 0x1.4p-19f : 0x1p-17f) + size * 0x1p-22f + 0x1p-24f;
-            unsure = high > -INFINITY && low - high <= 2.0f * err;
+            unsure = high > -INFINITY && !(low - high > 2.0f * err);  // (ranks that overflow differ by NaN)
         }
         if (exact)  // the scores were for the groups' ranks
 #pragma unroll

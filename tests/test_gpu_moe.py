@@ -306,6 +306,21 @@ def test_route_key_left_out_with_a_large_score(experts, score, p):
         assert torch.equal(r.experts.long(), want)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("experts,groups", [(32, 4), (256, 8), (60, 5)])
+def test_route_group_ranks_past_fp32(score, experts, groups):
+    """Groups whose two best keys add up to more than fp32 holds."""
+    per = experts // groups
+    bias = torch.zeros(experts)
+    for g in range(groups):
+        bias[g * per], bias[g * per + 1] = (2.0 + 0.1 * g) * 1e38, (1.9 + 0.1 * g) * 1e38
+    x = rnd(70, experts, seed=31)
+    for topk_groups in (1, groups - 1):
+        for k in (1, 2):
+            check_route(x, k, score=score, bias=bias, num_groups=groups, topk_groups=topk_groups)
+            check_route(x, k, score=score, bias=-bias, num_groups=groups, topk_groups=topk_groups)
+
+
 # ------------------------------------------------------------------ dispatch and combine
 
 def a_plan(tokens, experts, k, seed=0, masked=0.0):
