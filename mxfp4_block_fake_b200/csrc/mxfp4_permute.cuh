@@ -140,8 +140,10 @@ __global__ void __launch_bounds__(NTHREADS) dispatch_quant_kernel(const Dispatch
 // per word (4 words), E4M3 bytes of 4 per word (8 words). E2M1: the hardware
 // convert rounds to nearest with ties to even, the codebook sends ties up; a
 // tie is one of the fp32 values with at most two fraction bits, so those get
-// one more in their last place first, which moves codes themselves nowhere.
-// y + 0 turns -0 into +0 (the codebook's sign rule).
+// one more in their last place first, which moves codes themselves nowhere
+// (zeros and what lies above 8, infinities among it, are left alone). The
+// quotient y is rounded before 0 is added, so that every -0, one that
+// underflowed too, becomes +0 (the codebook's sign rule).
 template <int FMT, int N>
 __device__ __forceinline__ void quant_block(const uint32_t (&x)[32], const BP& p, uint32_t (&code)[N])
 {
@@ -163,8 +165,9 @@ __device__ __forceinline__ void quant_block(const uint32_t (&x)[32], const BP& p
             float y[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const uint32_t b = __float_as_uint(__fmaf_rn(__uint_as_float(x[8 * i + j]), p.inv, 0.0f));
-                y[j] = __uint_as_float(b | ((b & 0x1FFFFFu) == 0u ? 1u : 0u));
+                const uint32_t b = __float_as_uint(__fadd_rn(__fmul_rn(__uint_as_float(x[8 * i + j]), p.inv), 0.0f));
+                const bool tie = (b & 0x1FFFFFu) == 0u && (b & 0x7FFFFFFFu) - 1u < 0x40FFFFFFu;
+                y[j] = __uint_as_float(b | (tie ? 1u : 0u));
             }
             uint32_t w;
             asm("{\n\t.reg .b8 q0, q1, q2, q3;\n\t"

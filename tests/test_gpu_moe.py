@@ -452,6 +452,31 @@ def test_dispatch_fp32_values_beside_the_ties():
         assert np.array_equal(r.codes.cpu().numpy(), O.qdq_rowwise(x.numpy(), 32, 6.0, code)["codes"])
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("cols", [32, 64, 96, 77])
+def test_dispatch_values_whose_codes_underflow(dtype, cols):
+    """Negative values so far below a block's largest that their quotient by
+    the scale rounds to zero (code 0, as in the quantiser), or nearly does, and
+    scale factors whose quotients exceed fp32."""
+    tops = [100.0, 6.0, 1e34, 1e37, 3.0e38, 2.0 ** 100, 2.0 ** -100, 2.0 ** 17, 2.0 ** 20]
+    tiny = [2.0 ** -149, 2.0 ** -133, 2.0 ** -140, 1e-39, 2.0 ** -126, 1e-20, 1e-10, 0.0]
+    x = torch.zeros(len(tops) * len(tiny), cols, dtype=torch.float64)
+    for i, top in enumerate(tops):
+        for j, low in enumerate(tiny):
+            row = x[i * len(tiny) + j]
+            row[0::32] = top
+            row[1::32], row[2::32], row[3::32], row[4::32] = -low, low, -top * 2.0 ** -126, -top * 2.0 ** -3
+            row[5::32], row[6::32] = -3 * low, -0.0
+    x = x.float().to(DT[dtype])
+    rows = torch.arange(x.shape[0], dtype=torch.int32).view(-1, 1)
+    bits = x.view(torch.int16).numpy().view(np.uint16) if dtype == "bf16" else x.numpy()
+    for mode, code, factor in (("page", O.SCALE_PAGE, 6.0), ("floor", O.SCALE_FLOOR, 6.0), ("page", O.SCALE_PAGE, 3.3e38), ("page", O.SCALE_PAGE, 1e-30)):
+        r = ops.mxfp4_moe_dispatch(x.cuda(), rows.cuda(), emit_values=False, emit_codes=True, scale_mode=mode, scale_factor=factor)
+        assert np.array_equal(r.codes.cpu().numpy(), O.qdq_rowwise(bits, 32, factor, code)["codes"]), (mode, factor)
+    r = ops.mxfp4_moe_dispatch(x.cuda(), rows.cuda(), emit_values=False, emit_codes=True, elem_format="e4m3", scale_mode="floor")
+    assert np.array_equal(r.codes.cpu().numpy(), O.qdq8_rowwise(bits)["codes"])
+
+
 def test_dispatch_skips_rows_outside_and_strides():
     x = rnd(10, 100, seed=4, dtype=torch.bfloat16).cuda()[:, 1:97]
     rows = torch.arange(20, dtype=torch.int32).view(10, 2)
