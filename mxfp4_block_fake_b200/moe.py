@@ -176,7 +176,8 @@ class MXFP4MoE(nn.Module):
     Parameters: router [experts, cols]; w1 [experts, 2 hidden, cols], whose rows
     are gate and up rows in turn; w2 [experts, cols, hidden]. cols and hidden
     are multiples of 64. balance (with balance=True) is a buffer added to the
-    scores for the choice only; update_balance moves it against the load.
+    scores for the choice only; update_balance moves it against the load. It
+    stays float32 when the layer is cast or loaded.
 
     With gradients enabled the forward quantises the weights each call. For
     serving, lay_out() quantises them once, and forwards without gradients use
@@ -196,7 +197,7 @@ class MXFP4MoE(nn.Module):
         self.router = nn.Parameter(torch.randn(experts, cols, **kw) * cols ** -0.5)
         self.w1 = nn.Parameter(torch.randn(experts, 2 * hidden, cols, **kw) * cols ** -0.5)
         self.w2 = nn.Parameter(torch.randn(experts, cols, hidden, **kw) * hidden ** -0.5)
-        self.register_buffer("balance", torch.zeros(experts, device=device) if balance else None)
+        self.register_buffer("balance", torch.zeros(experts, dtype=torch.float32, device=device) if balance else None)
         self._laid_out = None
 
     def lay_out(self) -> "MXFP4MoE":
@@ -214,7 +215,16 @@ class MXFP4MoE(nn.Module):
 
     def _apply(self, fn, recurse=True):
         self._laid_out = None  # moved or cast: the copy is of the old weights
-        return super()._apply(fn, recurse)
+        balance = self.balance
+        super()._apply(fn, recurse)
+        if balance is not None and self.balance.dtype != torch.float32:  # cast with the weights: its fp32 value again
+            self.balance = balance.to(self.balance.device)
+        return self
+
+    def _load_from_state_dict(self, *args, **kw):
+        super()._load_from_state_dict(*args, **kw)
+        if self.balance is not None:
+            self.balance = self.balance.float()  # (assigned, it may be of another type)
 
     @torch.no_grad()
     def update_balance(self, counts: torch.Tensor, rate: float = 1e-3) -> None:

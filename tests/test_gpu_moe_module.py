@@ -145,6 +145,31 @@ def test_laid_out_copy_is_not_used_for_changed_weights(change):
             assert torch.equal(other(x), got)
 
 
+@pytest.mark.parametrize("build", ["method", "to", "default dtype"])
+def test_balance_stays_fp32(build):
+    """The balance is a sum of small steps and the routing's fp32 bias: casting the layer casts the weights only."""
+    torch.manual_seed(5)
+    dtype = torch.get_default_dtype()
+    try:
+        if build == "default dtype":
+            torch.set_default_dtype(torch.bfloat16)
+        m = MXFP4MoE(64, 64, 4, 2, balance=True, device="cuda", dtype=torch.bfloat16 if build == "default dtype" else torch.float32)
+    finally:
+        torch.set_default_dtype(dtype)
+    steps = torch.tensor([1.0, -1.0, 1.0, 1.0], device="cuda") * 1.0009765625   # not a bf16 value
+    m.balance += steps
+    m = m.bfloat16() if build == "method" else m.to(torch.bfloat16)
+    assert m.w1.dtype == torch.bfloat16 and m.balance.dtype == torch.float32 and torch.equal(m.balance, steps)
+    x = rnd(20, 64, seed=1, dtype=torch.bfloat16)
+    out, counts = m(x, return_counts=True)
+    out.sum().backward()
+    m.update_balance(torch.tensor([1, 9, 1, 1], device="cuda"))
+    assert torch.equal(m.balance, steps + 1e-3 * torch.tensor([1.0, -1.0, 1.0, 1.0], device="cuda"))
+    m.load_state_dict({n: v.bfloat16() for n, v in m.state_dict().items()}, assign=True)
+    m(x)
+    assert m.cpu().balance.device.type == "cpu" and m.balance.dtype == torch.float32 and "balance" in m.state_dict()
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("scale_mode", ["page", "floor"])
 def test_expert_operands(dtype, scale_mode):
