@@ -181,8 +181,11 @@ class MXFP4MoE(nn.Module):
 
     With gradients enabled the forward quantises the weights each call. For
     serving, lay_out() quantises them once, and forwards without gradients use
-    that copy until a weight is changed, replaced or moved (in-place changes as
-    autograd counts them; call it again after others, such as through .data)."""
+    that copy until a weight is loaded, changed, replaced or moved, or the scale
+    rule changes (in-place changes as autograd counts them; call it again after
+    others, such as through .data or by a replayed graph). A copy of the layer
+    starts without one, and weights made in inference mode, whose changes are
+    not counted, are refused."""
 
     def __init__(self, cols: int, hidden: int, experts: int, k: int, *, score: str = "softmax", num_groups: int = 1,
                  topk_groups: int | None = None, renormalize: bool = True, scale: float = 1.0, balance: bool = False,
@@ -202,16 +205,25 @@ class MXFP4MoE(nn.Module):
 
     def lay_out(self) -> "MXFP4MoE":
         """Quantises the experts' weights for serving."""
+        if self.w1.is_inference() or self.w2.is_inference():
+            raise RuntimeError("weights made in inference mode cannot be laid out: their changes are not counted")
         q = dict(scale_factor=self.scale_factor, scale_mode=self.scale_mode)
-        self._laid_out = (moe_expert_operands(self.w1, **q)[:2], moe_expert_operands(self.w2, **q)[:2], self._weights())
+        self._laid_out = (moe_expert_operands(self.w1, **q)[:2], moe_expert_operands(self.w2, **q)[:2], (self.w1, self.w2), self._changes())
         return self
 
-    def _weights(self):
-        """The experts' weights with their counts of in-place changes."""
-        return [(w, -1 if w.is_inference() else w._version) for w in (self.w1, self.w2)]
+    def _changes(self):
+        """The storage and the count of in-place changes of the experts' weights, and the scale rule."""
+        weights = [(w.data_ptr(), -1 if w.is_inference() else w._version) for w in (self.w1, self.w2)]
+        return weights, self.scale_factor, self.scale_mode
 
     def _copy_is_current(self) -> bool:
-        return self._laid_out is not None and all(a is b and i == j for (a, i), (b, j) in zip(self._laid_out[2], self._weights()))
+        if self._laid_out is None:
+            return False
+        _, _, (w1, w2), changes = self._laid_out
+        return w1 is self.w1 and w2 is self.w2 and changes == self._changes()
+
+    def __getstate__(self):
+        return {**self.__dict__, "_laid_out": None}  # a copy's weights count their changes from 0 again
 
     def _apply(self, fn, recurse=True):
         self._laid_out = None  # moved or cast: the copy is of the old weights
@@ -222,6 +234,7 @@ class MXFP4MoE(nn.Module):
         return self
 
     def _load_from_state_dict(self, *args, **kw):
+        self._laid_out = None
         super()._load_from_state_dict(*args, **kw)
         if self.balance is not None:
             self.balance = self.balance.float()  # (assigned, it may be of another type)
@@ -245,7 +258,7 @@ class MXFP4MoE(nn.Module):
             h = moe_grouped_linear(moe_dispatch(x2, r), self.w1, r.counts, activation="swiglu", check=False, **q)
             y = moe_grouped_linear(h, self.w2, r.counts, check=False, **q)
         else:
-            (c1, s1), (c2, s2), _ = self._laid_out
+            (c1, s1), (c2, s2), *_ = self._laid_out
             d = ops.mxfp4_moe_dispatch(x2, r.rows, emit_values=False, emit_codes=True, **q)
             h = ops.mxfp4_grouped_linear(d.codes, d.scales, c1, s1, r.counts, k=x2.shape[1], group_list_type=1,
                                          activation="swiglu", out_dtype=x2.dtype, check=False).y

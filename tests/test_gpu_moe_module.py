@@ -3,6 +3,9 @@ gradients against autograd of the same layer in 64 bits on the fake-quantised
 values, and the serving form against the training one."""
 from __future__ import annotations
 
+import copy
+import pickle
+
 import pytest
 import torch
 
@@ -143,6 +146,50 @@ def test_laid_out_copy_is_not_used_for_changed_weights(change):
         assert torch.equal(m.lay_out()(x), got)
         if change != "step":
             assert torch.equal(other(x), got)
+
+
+@pytest.mark.parametrize("how", ["deepcopy", "pickle", "parent", "data", "rule"])
+def test_laid_out_copy_of_other_weights_is_not_used(how):
+    """Copies of a laid-out layer whose count of changes happens to be the same
+    again, weights exchanged below autograd, and another scale rule."""
+    torch.manual_seed(4)
+    a, b, m = (MXFP4MoE(64, 128, 4, 2, device="cuda") for _ in range(3))
+    x = rnd(30, 64, seed=3, dtype=torch.bfloat16)
+    with torch.no_grad():
+        m.load_state_dict(a.state_dict())
+        m.lay_out()
+        old = m(x)
+        if how == "deepcopy":
+            m = copy.deepcopy(m)
+            m.load_state_dict(b.state_dict())
+        elif how == "pickle":
+            m = pickle.loads(pickle.dumps(m))
+            m.load_state_dict(b.state_dict())
+        elif how == "parent":
+            torch.nn.ModuleList([m]).load_state_dict(torch.nn.ModuleList([b]).state_dict())
+        elif how == "data":
+            m.router.data, m.w1.data, m.w2.data = b.router.data.clone(), b.w1.data.clone(), b.w2.data.clone()
+        else:
+            m.scale_mode = "floor"
+        got = m(x)
+        assert not torch.equal(got, old)
+        assert torch.equal(m.lay_out()(x), got)
+        if how != "rule":
+            assert torch.equal(b(x), got)
+
+
+def test_inference_tensors_are_not_laid_out():
+    """Their changes leave no trace, so a copy of them could not be known to be current."""
+    torch.manual_seed(6)
+    x = rnd(30, 64, seed=3, dtype=torch.bfloat16)
+    with torch.inference_mode():
+        m, other = (MXFP4MoE(64, 128, 4, 2, device="cuda") for _ in range(2))
+        with pytest.raises(RuntimeError, match="inference"):
+            m.lay_out()
+        m(x)
+        for p, q in zip(m.parameters(), other.parameters()):
+            p.copy_(q)
+        assert torch.equal(m(x), other(x))
 
 
 @pytest.mark.parametrize("build", ["method", "to", "default dtype"])
