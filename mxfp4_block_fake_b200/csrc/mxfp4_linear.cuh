@@ -832,6 +832,15 @@ __global__ void __launch_bounds__(NTHREADS, 4) linear_bwd_kernel(const LnBwdArgs
     }
 }
 
+// The status of a call whose matrices are empty: the list is checked all the same.
+__global__ void __launch_bounds__(NTHREADS) linear_list_kernel(const LnBwdArgs a)
+{
+    extern __shared__ __align__(16) int32_t lb_dyn[];
+    const int64_t units = ln_plan<LB_ROWS>(a, lb_dyn, lb_dyn + a.num_groups + 1);
+    if (threadIdx.x == 0)
+        *a.status = units >= 0 ? MXFP4_OK : MXFP4_EINVAL;
+}
+
 // grad_bias[g][c] = the sum of the group's units, in order. Grid: column
 // blocks x groups.
 __global__ void __launch_bounds__(NTHREADS) linear_bias_kernel(const LnBwdArgs a)

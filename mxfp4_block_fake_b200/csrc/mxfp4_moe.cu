@@ -554,9 +554,23 @@ static mxfp4_status check_linear(const mxfp4_linear_args* A)
     return MXFP4_OK;
 }
 
-static mxfp4_status zero_status(int32_t* status, cudaStream_t s)
+// The status of a call with nothing to multiply: its list's alone.
+static mxfp4_status list_status(const mxfp4_linear_args* A, cudaStream_t s)
 {
-    return status ? launched(cudaMemsetAsync(status, 0, sizeof(int32_t), s)) : MXFP4_OK;
+    if (!aligned(A->status, 4))
+        return MXFP4_EINVAL;
+    if (!A->status)
+        return MXFP4_OK;
+    if (!A->group_list)
+        return launched(cudaMemsetAsync(A->status, 0, sizeof(int32_t), s));
+    LnBwdArgs b;
+    memset(&b, 0, sizeof(b));
+    b.group_list = A->group_list;
+    b.status = A->status;
+    b.m = A->m;
+    b.num_groups = (int32_t)A->num_groups;
+    b.gl_type = A->group_list_type;
+    return launch1((const void*)linear_list_kernel, 1, NTHREADS, (size_t)(2 * (A->num_groups + 1)) * sizeof(int32_t), b, s);
 }
 
 static mxfp4_status run_linear(const mxfp4_linear_args* A, cudaStream_t s)
@@ -576,7 +590,7 @@ static mxfp4_status run_linear(const mxfp4_linear_args* A, cudaStream_t s)
     if (A->ld_y < width || (A->residual && A->ld_res < width) || (A->preact && A->ld_preact < A->n))
         return MXFP4_EINVAL;
     if (A->m == 0 || A->n == 0)
-        return zero_status(A->status, s);
+        return list_status(A, s);
     if (!A->a || !A->b || !A->a_scales || !A->b_scales || !A->y)
         return MXFP4_EINVAL;
     if (A->lda < kb || A->ldb < kb || A->lda % 16 != 0 || A->ldb % 16 != 0 || !aligned(A->a, 16) || !aligned(A->b, 16) ||
@@ -627,7 +641,7 @@ static mxfp4_status run_linear_bwd(const mxfp4_linear_args* A, cudaStream_t s)
     if (A->ld_y < width || A->ld_preact < A->n || A->ld_grad < A->n)
         return MXFP4_EINVAL;
     if (A->n == 0)
-        return zero_status(A->status, s);
+        return list_status(A, s);
     if (A->m > 0 && (!A->grad_out || !A->preact || !A->grad_preact))
         return MXFP4_EINVAL;
     if (!aligned(A->grad_out, esz) || !aligned(A->preact, esz) || !aligned(A->grad_preact, esz) || !aligned(A->grad_bias, 4) ||

@@ -778,6 +778,32 @@ def test_linear_invalid_lists():
             ops.mxfp4_grouped_linear_bwd(rnd(50, 64).cuda(), rnd(50, 64).cuda(), gl, group_list_type=kind)
 
 
+@pytest.mark.parametrize("m,n", [(0, 64), (50, 0), (0, 0)])
+def test_linear_lists_of_empty_matrices(m, n):
+    """A list is checked whatever there is to multiply, forward and backward alike."""
+    k = 128
+    a = torch.zeros(m, k // 2, dtype=torch.uint8, device="cuda")
+    sa = torch.zeros(ops.scales_row_bytes(m, k, 32, "mma"), dtype=torch.uint8, device="cuda")
+    b = torch.zeros(2, n, k // 2, dtype=torch.uint8, device="cuda")
+    sb = torch.zeros(2 * ops.scales_row_bytes(n, k, 32, "mma"), dtype=torch.uint8, device="cuda")
+    z = torch.zeros(m, n, device="cuda")
+    for sizes, kind, good in (([0, 0], 1, True), ([0, 0], 0, True), ([m, 0], 1, True), ([m, m], 0, True), ([m, 1], 1, False), ([0, -1], 1, False),
+                              ([-1, 1], 1, False), ([m + 1, m + 1], 0, False), ([1, 0], 0, False), ([2 ** 40, 0], 1, False)):
+        gl = torch.tensor(sizes, dtype=torch.int64, device="cuda")
+        calls = (lambda **kw: ops.mxfp4_grouped_linear(a, sa, b, sb, gl, k=k, group_list_type=kind, **kw),
+                 lambda **kw: ops.mxfp4_grouped_linear_bwd(z, z, gl, group_list_type=kind, **kw))
+        for call in calls:
+            if good:
+                call()
+            else:
+                with pytest.raises(MXFP4ArgumentError):
+                    call()
+        assert int(calls[0](check=False).status) == (0 if good else 1)
+    ops.mxfp4_grouped_linear(a, sa, b[0], sb[: sb.numel() // 2], k=k)
+    _, gb = ops.mxfp4_grouped_linear_bwd(z, z)
+    assert not gb.any()
+
+
 def test_invalid_lists_of_large_linears():
     a, sa = operand(4096, 2048, "e2m1", 1)
     b, sb = operand(4608, 2048, "e2m1", 2)

@@ -150,6 +150,14 @@ def test_linear_bwd_refuses_on_the_host(abi, kw, expected):
     assert abi.mxfp4_grouped_linear_bwd(a, None) == expected
 
 
+def test_empty_matrices_are_checked_like_others(abi):
+    for empty in (dict(m=0), dict(n=0)):
+        for kw in (dict(status=P + 2), dict(group_list=P + 4), dict(num_groups=0), dict(group_list_type=2)):
+            assert abi.mxfp4_grouped_linear(linear(abi, **{**empty, **kw}), None) == 1
+            a = linear(abi, **{**dict(grad_out=P, preact=P, grad_preact=P), **empty, **kw})
+            assert abi.mxfp4_grouped_linear_bwd(a, None) == 1
+
+
 def test_nothing_to_do_is_ok_without_a_device(abi):
     assert abi.mxfp4_moe_route_bwd(route(abi, tokens=0, ld_grad=16), None) == 0
     assert abi.mxfp4_moe_combine(move(abi, tokens=0, rows=None), None) == 0
