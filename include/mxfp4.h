@@ -608,10 +608,11 @@ mxfp4_status mxfp4_moe_combine_bwd(const mxfp4_moe_move_args* args, mxfp4_stream
  * preact [m][n], grad_preact [m][n] (ld_grad; d_dtype; gated: d gate = grad up
  * silu'(gate), d up = grad silu(gate)) and, optionally, grad_bias fp32
  * [groups][n], the sums of the unrounded grad_preact over each group's rows
- * (0 for an empty group). The residual's gradient is grad_out; the
- * operands' gradients are grouped GEMMs of grad_preact. workspace:
- * mxfp4_grouped_linear_workspace(m, n, num_groups) bytes, 4-byte aligned,
- * when grad_bias is given (num_groups 1 without a group list). a, b and k are
+ * (0 for an empty group, and for every group of an invalid list). The
+ * residual's gradient is grad_out; the operands' gradients are grouped GEMMs
+ * of grad_preact. workspace: mxfp4_grouped_linear_workspace(m, n, num_groups)
+ * bytes, 4-byte aligned, when grad_bias is given (num_groups 1 without a group
+ * list). a, b and k are
  * not used. Rows behind the last group are left as they were.
  */
 typedef struct mxfp4_linear_args {

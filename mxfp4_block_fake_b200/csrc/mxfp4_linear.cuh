@@ -841,7 +841,7 @@ __global__ void __launch_bounds__(NTHREADS) linear_list_kernel(const LnBwdArgs a
         *a.status = units >= 0 ? MXFP4_OK : MXFP4_EINVAL;
 }
 
-// grad_bias[g][c] = the sum of the group's units, in order. Grid: column
+// grad_bias[g][c] = the sum of the group's units, in order (0 for an invalid list). Grid: column
 // blocks x groups.
 __global__ void __launch_bounds__(NTHREADS) linear_bias_kernel(const LnBwdArgs a)
 {
@@ -851,15 +851,14 @@ __global__ void __launch_bounds__(NTHREADS) linear_bias_kernel(const LnBwdArgs a
     // (started early, its waiting CTAs took room from linear_bwd_kernel's: 94 against 78 us)
     const bool ok = ln_plan<LB_ROWS>(a, s_tpre, s_rst) >= 0;
     wait_for_prerequisite();
-    if (!ok)
-        return;
     const int64_t c = (int64_t)blockIdx.x * NTHREADS + threadIdx.x;
     if (c >= a.n)
         return;
     for (int g = blockIdx.y; g < a.num_groups; g += gridDim.y) {
         float v = 0.0f;
+        const int end = ok ? s_tpre[g + 1] : s_tpre[g];  // an invalid list: no rows, and no partial sums were written
 #pragma unroll 4
-        for (int u = s_tpre[g]; u < s_tpre[g + 1]; ++u)
+        for (int u = s_tpre[g]; u < end; ++u)
             v += a.ws[(int64_t)u * a.n + c];
         a.grad_bias[(int64_t)g * a.n + c] = v;
     }

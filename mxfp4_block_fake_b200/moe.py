@@ -162,8 +162,9 @@ def moe_grouped_linear(x: torch.Tensor, weight: torch.Tensor, counts: torch.Tens
     (x in expert order; rows behind them give zero). weight [E, n, k], k a
     multiple of 64; bias float32 [E, n]; activation as in
     ops.mxfp4_grouped_linear. check synchronises and raises for counts that are
-    negative or exceed the rows (without it such counts give zeros); counts of
-    moe_route need none. The backward copies counts to the host."""
+    negative or exceed the rows (without it such counts give zeros, and zero
+    gradients); counts of moe_route need none. The backward copies counts to
+    the host."""
     if weight.ndim != 3 or x.ndim != 2 or weight.shape[2] != x.shape[1] or weight.dtype != x.dtype:
         raise ValueError("x must be [rows, k] and weight [experts, n, k], of one dtype")
     return _GroupedLinear.apply(x, weight, bias, counts, activation, scale_factor, scale_mode, bool(check))

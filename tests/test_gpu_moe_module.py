@@ -238,6 +238,20 @@ def test_counts_that_do_not_fit(counts):
     assert not moe.moe_grouped_linear(x, w, c, check=False).any()
 
 
+@pytest.mark.parametrize("counts", [[3, 4], [-1, 2], [7, 0]])
+@pytest.mark.parametrize("rows", [6, 40])
+def test_gradients_for_counts_that_do_not_fit(counts, rows):
+    """Results are zeros without a check, and so is every gradient, the bias's too."""
+    counts = [c * rows // 6 + (1 if c == 7 else 0) for c in counts]
+    x, w, b = (v.requires_grad_(True) for v in (rnd(rows, 64, seed=7), rnd(2, 8, 64, seed=8), rnd(2, 8, seed=9)))
+    y = moe.moe_grouped_linear(x, w, torch.tensor(counts).cuda(), b, check=False)
+    for _ in range(4):      # what the allocator hands out next is not zero
+        torch.full((2, 8), 7.0, device="cuda")
+    y.sum().backward()
+    for v in (x, w, b):
+        assert not v.grad.any()
+
+
 def test_optimiser_steps_run():
     torch.manual_seed(2)
     m = MXFP4MoE(64, 64, 4, 2, device="cuda", dtype=torch.float32)
