@@ -720,7 +720,9 @@ int64_t mxfp4_moe_dispatch_workspace(int64_t tokens, int32_t k, int64_t cols, in
     // by 4-byte stores the scales cost about 8 us per million words, the second
     // kernel about 3 us and a sixth of that
     const int64_t words = (cols + 127) / 128;
-    return tokens * k * words < (int64_t)1 << 19 ? 0 : (tokens * words + row_count) * 4;
+    if (tokens * k * words < (int64_t)1 << 19 || (words + SG_WORDS - 1) / SG_WORDS > 65535)  // (its grid's second dimension)
+        return 0;
+    return (tokens * words + row_count) * 4;
 }
 
 mxfp4_status mxfp4_moe_dispatch(const mxfp4_moe_move_args* args, mxfp4_stream_t stream)

@@ -928,6 +928,20 @@ def test_rows_past_32_bits():
         assert torch.equal(gy[int(rows[i, 0])], x[i])
 
 
+def test_dispatch_of_a_very_wide_row():
+    """More scale columns than one launch of the scales' second kernel has room for."""
+    cols = 65536 * 32 * 128                      # one block row of that kernel too many
+    x = torch.randn(1 << 16, device="cuda").bfloat16().repeat(cols >> 16).view(1, cols)
+    rows = torch.tensor([[1, 0]], dtype=torch.int32, device="cuda")
+    r = ops.mxfp4_moe_dispatch(x, rows, emit_values=False, emit_codes=True)
+    q = ops.mxfp4_qdq_fwd(x.view(4096, -1), emit_values=False, emit_codes=True)      # the same blocks as shorter rows
+    assert torch.equal(r.codes[0], q.codes_row.view(-1)) and torch.equal(r.codes[1], q.codes_row.view(-1))
+    got, want = r.scales.view(-1, 512), q.scales_row.view(-1, 4)
+    # word 4 (row % 32) + row // 32 of an atom: rows 0 and 1, the others padding
+    assert torch.equal(got[:, :4], want) and torch.equal(got[:, 16:20], want)
+    assert not got[:, 4:16].any() and not got[:, 20:].any()
+
+
 def test_results_past_32_bits():
     """2.4e9 results of a product; rows of a slice by themselves give the same bytes."""
     m, n, k = 300032, 8192, 64
