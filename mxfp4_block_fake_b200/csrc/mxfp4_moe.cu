@@ -554,6 +554,19 @@ static mxfp4_status check_linear(const mxfp4_linear_args* A)
     return MXFP4_OK;
 }
 
+static mxfp4_status check_product(const mxfp4_linear_args* A)
+{
+    const mxfp4_status st = check_linear(A);
+    if (st != MXFP4_OK)
+        return st;
+    const bool e2 = A->elem_format == MXFP4_ELEM_E2M1;
+    if (!e2 && A->elem_format != MXFP4_ELEM_E4M3)
+        return MXFP4_EINVAL;
+    if (A->k < 1 || A->k % (e2 ? 64 : 32) != 0)
+        return MXFP4_EINVAL;
+    return A->k > INT32_MAX ? MXFP4_EUNSUPPORTED : MXFP4_OK;
+}
+
 // The status of a call with nothing to multiply: its list's alone.
 static mxfp4_status list_status(const mxfp4_linear_args* A, cudaStream_t s)
 {
@@ -575,16 +588,10 @@ static mxfp4_status list_status(const mxfp4_linear_args* A, cudaStream_t s)
 
 static mxfp4_status run_linear(const mxfp4_linear_args* A, cudaStream_t s)
 {
-    const mxfp4_status st = check_linear(A);
+    const mxfp4_status st = check_product(A);
     if (st != MXFP4_OK)
         return st;
     const bool e2 = A->elem_format == MXFP4_ELEM_E2M1, gated = A->activation == MXFP4_ACT_SWIGLU;
-    if (!e2 && A->elem_format != MXFP4_ELEM_E4M3)
-        return MXFP4_EINVAL;
-    if (A->k < 1 || A->k % (e2 ? 64 : 32) != 0)
-        return MXFP4_EINVAL;
-    if (A->k > INT32_MAX)
-        return MXFP4_EUNSUPPORTED;
     const int64_t kb = e2 ? A->k / 2 : A->k, width = gated ? A->n / 2 : A->n;
     const size_t esz = A->d_dtype == MXFP4_F32 ? 4 : 2;
     if (A->ld_y < width || (A->residual && A->ld_res < width) || (A->preact && A->ld_preact < A->n))
@@ -747,7 +754,7 @@ mxfp4_status mxfp4_grouped_linear(const mxfp4_linear_args* args, mxfp4_stream_t 
 
 int64_t mxfp4_grouped_linear_fwd_workspace(const mxfp4_linear_args* args)
 {
-    if (check_linear(args) != MXFP4_OK || args->k < 0)
+    if (check_product(args) != MXFP4_OK)
         return -1;
     return linear_on_pairs(args) ? scale_tiles_bytes(args->m, args->k, args->group_list ? args->num_groups : 1) : 0;
 }

@@ -185,6 +185,13 @@ def test_workspace_sizes(abi):
     assert L.mxfp4_moe_dispatch_workspace(-1, 8, 7168, 1) == -1
 
 
+@pytest.mark.parametrize("kw", [dict(elem_format=2), dict(k=0), dict(k=-64), dict(k=7200), dict(elem_format=1, k=7184), dict(activation=5, n=4097),
+                                dict(num_groups=0), dict(m=-1), dict(k=2 ** 62), dict(n=2 ** 31), dict(m=2 ** 31), dict(num_groups=4097)])
+def test_forward_workspace_of_invalid_arguments(abi, kw):
+    a = linear(abi, **{**dict(m=8192, n=4096, k=7168, num_groups=8), **kw})
+    assert abi.mxfp4_grouped_linear_fwd_workspace(a) == -1
+
+
 def test_cpu_tensors_are_refused():
     from mxfp4_block_fake_b200 import ops
     x = torch.zeros(4, 64)
