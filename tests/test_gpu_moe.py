@@ -893,6 +893,28 @@ def test_linear_backward_large_values():
         assert torch.equal(gb.cpu(), gz.cpu())
 
 
+@pytest.mark.parametrize("m", [1, 40])
+def test_gelu_keeps_the_digits_of_small_results(m):
+    """z is the bias alone (zero operands). The mass below z is e t P(t): 8
+    roundings of P and its product with t (measured over the range in fp32), 5 of
+    t (a quotient within 2 units, a sum) of which at most 1.9 times pass on, e =
+    exp(-z^2 / 2) by an exponential within 2 + 1.173 z^2 / 2 units whose argument
+    rounds once (z^2 / 2), one product: below 24 + 1.7 z^2 roundings of itself.
+    What fp32 cannot hold as a normal number counts as 0."""
+    n, k = 8192, 64
+    z = torch.linspace(-13.0, 13.0, n)
+    code = lambda r: (torch.zeros(r, k // 2, dtype=torch.uint8, device="cuda"),  # noqa: E731
+                      torch.full((ops.scales_row_bytes(r, k, 32, "mma"),), 127, dtype=torch.uint8, device="cuda"))
+    got = ops.mxfp4_grouped_linear(*code(m), *code(n), k=k, bias=z.cuda(), activation="gelu", out_dtype=torch.float32).y
+    v = z.double()
+    mass, density = 0.5 * torch.special.erfc(-v / math.sqrt(2.0)), torch.exp(-v * v / 2) / math.sqrt(2 * math.pi)
+    for row in got:
+        close(row, v * mass, ((25 + 1.7 * v * v) * U32 * mass + 2.0 ** -126) * v.abs(), "gelu")
+    gz, _ = ops.mxfp4_grouped_linear_bwd(torch.ones(1, n, device="cuda"), z.view(1, n).cuda(), activation="gelu")
+    bound = (25 + 1.7 * v * v) * U32 * (mass + v.abs() * density) + 2.0 ** -126 * (1 + v.abs())
+    close(gz[0], mass + v * density, bound, "slope")
+
+
 def test_linear_backward_strided():
     z, g = rnd(70, 100, seed=1).cuda(), rnd(70, 60, seed=2).cuda()
     one = ops.mxfp4_grouped_linear_bwd(g[:, 7:53], z[:, 3:95], activation="swiglu")
