@@ -258,10 +258,10 @@ static mxfp4_status run_dispatch(const mxfp4_moe_move_args* A, cudaStream_t s)
         return st;
     const size_t esz = esize(A);
     const bool e4 = A->elem_format == MXFP4_ELEM_E4M3;
-    if (!A->values && !A->codes)
-        return MXFP4_EINVAL;
     if (A->ld_tokens < A->cols || (A->values && A->ld_rows < A->cols))
         return MXFP4_EINVAL;
+    if (!A->values && !A->codes)  // (outputs without an element may have no address)
+        return A->row_count == 0 || A->cols == 0 ? MXFP4_OK : MXFP4_EINVAL;
     if (A->codes) {
         if (!A->scales || (A->elem_format != MXFP4_ELEM_E2M1 && !e4))
             return MXFP4_EINVAL;
@@ -380,10 +380,10 @@ static mxfp4_status run_combine_bwd(const mxfp4_moe_move_args* A, cudaStream_t s
     const size_t esz = esize(A);
     if (A->ld_out < A->cols || (A->grad_weights && A->ld_rows < A->cols) || (A->grad_rows && A->ld_grad_rows < A->cols))
         return MXFP4_EINVAL;
-    if (!A->grad_rows && !A->grad_weights)
-        return MXFP4_EINVAL;
     if (A->tokens == 0)
         return MXFP4_OK;
+    if (!A->grad_rows && !A->grad_weights)
+        return A->row_count == 0 || A->cols == 0 ? MXFP4_OK : MXFP4_EINVAL;
     if ((A->cols > 0 && !A->grad_out) || (A->grad_weights && A->row_count > 0 && A->cols > 0 && !A->y) ||
         !aligned(A->grad_out, esz) || !aligned(A->y, esz) || !aligned(A->grad_rows, esz) || !aligned(A->weights, 4) ||
         !aligned(A->grad_weights, 4))

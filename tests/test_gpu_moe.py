@@ -544,6 +544,23 @@ def test_combine_backward(dtype, tokens, k, cols):
     assert only[0] is None and torch.equal(only[1], gw)
 
 
+def test_moves_without_tokens_rows_or_columns():
+    i32 = dict(dtype=torch.int32, device="cuda")
+    for t, cols, n in ((0, 64, 0), (0, 64, 5), (3, 64, 0), (3, 0, 6)):
+        x, rows = torch.ones(t, cols, device="cuda"), torch.arange(2 * t, **i32).view(t, 2)
+        y, w = torch.ones(n, cols, device="cuda"), torch.ones(t, 2, device="cuda")
+        for kw in (dict(), dict(emit_values=False, emit_codes=True), dict(emit_codes=True)):
+            d = ops.mxfp4_moe_dispatch(x, rows, row_count=n, **kw)
+            assert d.values is None or d.values.shape == (n, cols)
+            if d.codes is not None:      # scales of rows behind the last are zero, those of rows that no index names undefined
+                words = d.scales.view(-1, 32, 4, 4)
+                assert not words[:, n:].any() and not words[:, :, 1:].any()
+        assert torch.equal(ops.mxfp4_moe_combine(y, rows, w, residual=x), x)
+        gy, gw = ops.mxfp4_moe_combine_bwd(x, y, rows, w)
+        assert gy.shape == (n, cols) and not gw.any()
+        assert ops.mxfp4_moe_combine_bwd(x, None, rows, w, grad_weights=False, row_count=n)[0].shape == (n, cols)
+
+
 # ------------------------------------------------------------------------------- linear
 
 def operand(rows, k, fmt, seed, lo=126, hi=129):

@@ -148,6 +148,19 @@ def test_laid_out_copy_is_not_used_for_changed_weights(change):
             assert torch.equal(other(x), got)
 
 
+@pytest.mark.parametrize("shape", [(0, 64), (2, 0, 64)])
+def test_module_without_tokens(shape):
+    m = MXFP4MoE(64, 64, 4, 2, device="cuda")
+    x = torch.zeros(shape, dtype=torch.bfloat16, device="cuda", requires_grad=True)
+    out, counts = m(x, return_counts=True)
+    assert out.shape == x.shape and not counts.any()
+    out.sum().backward()
+    assert x.grad.shape == x.shape and not any(p.grad.any() for p in m.parameters())
+    m.lay_out()
+    with torch.no_grad():
+        assert m(x).shape == x.shape
+
+
 @pytest.mark.parametrize("how", ["deepcopy", "pickle", "parent", "data", "rule"])
 def test_laid_out_copy_of_other_weights_is_not_used(how):
     """Copies of a laid-out layer whose count of changes happens to be the same

@@ -166,6 +166,16 @@ def test_nothing_to_do_is_ok_without_a_device(abi):
     assert abi.mxfp4_grouped_linear(linear(abi, m=0), None) == 0
 
 
+def test_outputs_without_an_element_need_no_address(abi):
+    assert abi.mxfp4_moe_dispatch(move(abi, tokens=0, row_count=0, rows=None), None) == 0
+    assert abi.mxfp4_moe_dispatch(move(abi, x=P, row_count=0), None) == 0
+    assert abi.mxfp4_moe_dispatch(move(abi, x=P, cols=0), None) == 0
+    assert abi.mxfp4_moe_dispatch(move(abi, x=P, row_count=0, ld_tokens=63), None) == 1
+    assert abi.mxfp4_moe_combine_bwd(move(abi, tokens=0, rows=None), None) == 0
+    assert abi.mxfp4_moe_combine_bwd(move(abi, grad_out=P, row_count=0), None) == 0
+    assert abi.mxfp4_moe_combine_bwd(move(abi, tokens=0, rows=None, ld_out=63), None) == 1
+
+
 def test_workspace_sizes(abi):
     L = abi.lib()
     assert L.mxfp4_moe_route_workspace(64, 256) == 0
