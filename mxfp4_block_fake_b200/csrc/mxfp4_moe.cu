@@ -26,10 +26,12 @@ namespace mxfp4 {
 static mxfp4_status launched(cudaError_t e) { return e == cudaSuccess ? MXFP4_OK : MXFP4_ECUDA; }
 
 // Lets `fn` be launched with `smem` bytes of dynamic shared memory; asked of the
-// runtime once per (kernel, device) and size above the last.
+// runtime once per (kernel, device) and size above the last. Without asking, 48 KB
+// are open to a kernel's static and dynamic shared memory together (the static part
+// starts at 1 KB; kernels with a large dynamic part here have at most 9 KB).
 static bool allow_smem(const void* fn, size_t smem)
 {
-    if (smem <= 48 * 1024)
+    if (smem <= 32 * 1024)
         return true;
     struct Entry {
         const void* fn;

@@ -7,6 +7,8 @@ the value. The bounds are written beside each check.
 from __future__ import annotations
 
 import math
+import subprocess
+import sys
 
 import numpy as np
 import pytest
@@ -15,6 +17,7 @@ import torch
 import oracle as O
 from mxfp4_block_fake_b200 import MXFP4ArgumentError, ops
 from tests import moe_ref as R
+from tests.conftest import ROOT
 
 pytestmark = pytest.mark.gpu
 
@@ -157,6 +160,23 @@ def test_route_choice_of_many_tokens(dtype, score, bias_kind, experts, groups, t
     r = ops.mxfp4_moe_route(x, k, score=score, bias=bias, num_groups=groups, topk_groups=topk_groups)
     # softmax in 64 bits may round two different logits' keys to one only where they are 2^-52 apart: none here
     assert torch.equal(r.experts.long(), want)
+
+
+def test_route_shared_memory_near_its_default_limit():
+    """Calls whose shared memory is just below the size that a kernel may have
+    without asking for more, each the first of its kernel in a new process."""
+    code = """
+import torch
+from mxfp4_block_fake_b200 import ops
+for dtype in (torch.float32, torch.bfloat16):
+    for score in ("softmax", "sigmoid"):
+        for experts, k in [(640, 24)] + [(e, k) for e in range(600, 700, 3) for k in (1, 16, 31)]:
+            x = torch.randn(70, experts, generator=torch.Generator().manual_seed(experts)).to(dtype).cuda()
+            want = x.sort(dim=1, descending=True, stable=True).indices[:, :k]
+            assert torch.equal(ops.mxfp4_moe_route(x, k, score=score).experts.long(), want), (dtype, score, experts, k)
+"""
+    run = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0, run.stderr[-2000:]
 
 
 @pytest.mark.parametrize("tokens", [0, 1, 64, 65, 2048, 2049, 5000])
