@@ -184,10 +184,12 @@ __device__ __forceinline__ uint32_t round_bf16_bits(uint32_t b)
     return (b + 0x7FFFu + ((b >> 16) & 1u)) & 0xFFFF0000u;
 }
 
+// Volatile: the compiler takes an asm without it for arithmetic and may execute it
+// ahead of the condition that guards it, which reads outside the tensor.
 __device__ __forceinline__ uint4 ld_stream(const void* p)
 {
     uint4 r;
-    asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
         : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
         : "l"(p));
     return r;

@@ -1001,6 +1001,42 @@ def test_dispatch_of_a_very_wide_row():
     assert not got[:, 4:16].any() and not got[:, 20:].any()
 
 
+def at_the_end(t: torch.Tensor) -> torch.Tensor:
+    """A copy of t that ends where a block of the device's memory (2 MB pages) ends."""
+    size = t.numel() * t.element_size()
+    block = torch.empty((max(size, 1 << 25) + (1 << 21) - 1) >> 21 << 21, dtype=torch.uint8, device="cuda")
+    out = block[block.numel() - size:].view(t.dtype).view(t.shape)
+    out.copy_(t)
+    return out
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("cols", [8, 96, 256, 1000, 4096])
+def test_inputs_at_the_end_of_their_memory(dtype, cols):
+    """Nothing is read behind a tensor's last row, however little of the
+    threads' reach it fills: the results of the same calls elsewhere."""
+    torch.cuda.empty_cache()
+    t, k, n = 12, 5, 60
+    rows, _, counts = a_plan(t, 7, k)
+    x, y, z, g, gz = (rnd(r, c, seed=i, dtype=DT[dtype]).cuda() for i, (r, c) in enumerate(((t, cols), (n, cols), (n, cols), (t, cols), (n, cols // 2))))
+    lg, w = rnd(t, 64, seed=9, dtype=DT[dtype]).cuda(), rnd(t, k, seed=8).cuda()
+    rows, counts = rows.cuda(), counts.cuda()
+    chosen = ops.mxfp4_moe_route(lg, k).experts
+
+    def results(f):
+        x2, y2, z2, g2, gz2, lg2, w2, rows2 = (f(v) for v in (x, y, z, g, gz, lg, w, rows))
+        zero = lambda: torch.zeros(n, cols, dtype=DT[dtype], device="cuda")  # noqa: E731
+        r = ops.mxfp4_moe_route(lg2, k)
+        d = ops.mxfp4_moe_dispatch(x2, rows2, emit_codes=True)
+        return [r.weights, r.experts, d.values, d.codes, d.scales, ops.mxfp4_moe_combine(y2, rows2, w2, residual=x2),
+                *ops.mxfp4_moe_combine_bwd(g2, y2, rows2, w2, out=zero()), ops.mxfp4_moe_route_bwd(w2, lg2, chosen),
+                *ops.mxfp4_grouped_linear_bwd(gz2, z2, counts, group_list_type=1, activation="swiglu", out=zero()),
+                *ops.mxfp4_grouped_linear_bwd(y2, z2, counts, group_list_type=1, activation="gelu", out=zero())]
+
+    for a, b in zip(results(lambda v: v), results(at_the_end)):
+        assert torch.equal(a, b)
+
+
 def test_results_past_32_bits():
     """2.4e9 results of a product; rows of a slice by themselves give the same bytes."""
     m, n, k = 300032, 8192, 64
