@@ -364,8 +364,8 @@ __device__ __forceinline__ bool dual_unit_fast(const DualArgs& a, int row, int j
         float tlo, thi;
         upk2(fma2_rm(Y[i], INV2, pk2(2097152.0f, 2097152.0f)), tlo, thi);
         uint32_t elo, ehi;
-        asm("ld.shared.u32 %0, [%1];" : "=r"(elo) : "r"(__float_as_uint(tlo) * a.mul4 + lutb));
-        asm("ld.shared.u32 %0, [%1];" : "=r"(ehi) : "r"(__float_as_uint(thi) * a.mul4 + lutb));
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(elo) : "r"(__float_as_uint(tlo) * a.mul4 + lutb));
+        asm volatile("ld.shared.u32 %0, [%1];" : "=r"(ehi) : "r"(__float_as_uint(thi) * a.mul4 + lutb));
         cv[2 * i] = __uint_as_float(elo | ((sg[i] * a.mul16) & 0x80000000u));
         cv[2 * i + 1] = __uint_as_float(ehi | (sg[i] & 0x80000000u));
         float olo, ohi;
