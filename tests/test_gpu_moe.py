@@ -1037,6 +1037,25 @@ def test_inputs_at_the_end_of_their_memory(dtype, cols):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("fmt", ["e2m1", "e4m3"])
+@pytest.mark.parametrize("sizes,m,n,k", [([1, 2], 3, 130, 192), ([40, 0, 33], 80, 200, 320), ([2500, 1700], 4200, 2100, 2112)])
+def test_operands_at_the_end_of_their_memory(fmt, sizes, m, n, k):
+    torch.cuda.empty_cache()
+    a, sa = operand(m, k, fmt, 1)
+    parts = [operand(n, k, fmt, 2 + i, 117, 119) for i in range(len(sizes))]
+    gl = torch.tensor(sizes, dtype=torch.int64)
+    args = (a, sa, torch.stack([p[0] for p in parts]), torch.cat([p[1] for p in parts]), gl, rnd(len(sizes), n, seed=5), rnd(m, n // 2, seed=6))
+
+    def result(f):
+        a, sa, b, sb, gl, bias, res = (f(v.cuda()) for v in args)
+        r = ops.mxfp4_grouped_linear(a, sa, b, sb, gl, k=k, elem_format=fmt, group_list_type=1, bias=bias, activation="swiglu", residual=res,
+                                     out_dtype=torch.float32, out=ops.LinearResult(y=torch.zeros(m, n // 2, device="cuda"), preact=torch.zeros(m, n, device="cuda")))
+        return r.y, r.preact
+
+    for x, y in zip(result(lambda v: v), result(at_the_end)):
+        assert torch.equal(x, y)
+
+
 def test_results_past_32_bits():
     """2.4e9 results of a product; rows of a slice by themselves give the same bytes."""
     m, n, k = 300032, 8192, 64
