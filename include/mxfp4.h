@@ -466,7 +466,9 @@ mxfp4_status mxfp4_dual_level_qdq(const mxfp4_dual_level_args* args, mxfp4_strea
  *   workspace   mxfp4_moe_route_workspace(tokens, experts) bytes, 16-byte
  *               aligned (may be NULL when that is 0); its contents matter
  *               to this call only.
- * Limits: experts <= 1024, k <= 32, num_groups <= 32, tokens * k < 2^31.
+ * Limits: experts <= 1024, k <= 32, num_groups <= 32, tokens * k < 2^31. (k = 32
+ * selects every token twice, unless bf16 logits are compared as they are: about
+ * three times the time of k = 31.)
  *
  * mxfp4_moe_route_bwd: grad_logits [tokens][experts] (leading dimension
  * ld_grad, dtype as logits) from grad_weights fp32 [tokens][k], for the chosen
@@ -509,8 +511,8 @@ mxfp4_status mxfp4_moe_route_bwd(const mxfp4_moe_route_args* args, mxfp4_stream_
  * Dispatch and combine. rows int32 [tokens][k] is the index list of
  * mxfp4_moe_route: the row of each (token, slot) among row_count expert rows.
  * An index outside [0, row_count) is skipped; rows that no index names are
- * left as they were. The indices in range must differ from one another (an
- * index named twice receives one of the two rows).
+ * left as they were. The indices in range must differ from one another: a row
+ * named twice receives parts of either, not the same ones every time.
  *
  * mxfp4_moe_dispatch: row rows[t][j] of the outputs = row t of x,
  *   values      x's dtype, [row_count][cols], leading dimension ld_out, and / or

@@ -507,8 +507,10 @@ static mxfp4_status launch_linear2(const mxfp4_linear_args* A, const LnMaps& map
     return launch_after(fn, dim3((unsigned)(2 * (bound < pairs ? bound : pairs))), L2_THREADS, smem, args2, s);
 }
 
-// Whether a product goes to pairs of SMs (given the workspace). Groups that fill
-// 256-token tiles on average; tiles for most of the device (1024 x 4096 x 4096 31
+// Whether a product goes to pairs of SMs (given the workspace). Groups of 256 rows or
+// more on average, which leave tiles partly empty but still came faster on ragged ones
+// (65536 x 4096 x 7168, swiglu, 256 groups: equal sizes 995 against 1490 us, uniform
+// draws 1446 / 1900, log-normal 1406 / 1970; k = 2048 613 / 610 and 586 / 606); tiles for most of the device (1024 x 4096 x 4096 31
 // against the single-SM kernel's 24 us, 4096 x 4096 x 4096 57 / 63); and eight
 // stages along K, since its one accumulator waits for both CTAs' epilogues
 // (32768 x 4096 over 32 experts, E2M1, bf16 results: k = 1024 184 / 160 us, 2048 194 /

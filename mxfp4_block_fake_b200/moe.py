@@ -176,9 +176,10 @@ class MXFP4MoE(nn.Module):
 
     Parameters: router [experts, cols]; w1 [experts, 2 hidden, cols], whose rows
     are gate and up rows in turn; w2 [experts, cols, hidden]. cols and hidden
-    are multiples of 64. balance (with balance=True) is a buffer added to the
-    scores for the choice only; update_balance moves it against the load. It
-    stays float32 when the layer is cast or loaded.
+    are multiples of 64. The router's logits are formed in the layer's dtype, and
+    groups are ranked by their two best keys. balance (with balance=True) is a
+    buffer added to the scores for the choice only; update_balance moves it
+    against the load. It stays float32 when the layer is cast or loaded.
 
     With gradients enabled the forward quantises the weights each call. For
     serving, lay_out() quantises them once, and forwards without gradients use
